@@ -348,6 +348,163 @@ typedef struct smc_epilogue {
 int smc_forward_ex(smc_handle_t h, const void* feats, const void* W, void* out, int K, int cin,
                    int cout, int dtype, const smc_epilogue* ep, smc_stream_t stream);
 
+/*
+ * Layer norm over the channels of each feature row (trellis_sparse_mlx README,
+ * "What's in it": LayerNorm32, whose parameters and arithmetic are fp32
+ * whatever the rows' type):
+ *
+ *     out = (x - mean(x)) / sqrt(var(x) + eps) * gamma + beta
+ *
+ * with the row's mean and its (biased) variance about that mean.
+ *
+ * x, out      : device pointers, [n][c] of dtype; out may be x itself.
+ * gamma, beta : device pointers, float32 [c], or NULL (ones / zeros).
+ * n, c        : n >= 0 rows of c >= 1 channels.
+ * eps         : >= 0, added to the variance.
+ * Statistics and arithmetic are fp32; the result is rounded once to dtype.
+ * A row's result depends on that row alone (an infinite or NaN value makes
+ * its own row NaN and no other).  Asynchronous on stream; no workspace.
+ * Errors: SMC_ERR_INVALID (null or misaligned pointers, bad sizes, dtype or
+ * eps, out overlapping an input in any other way), SMC_ERR_UNSUPPORTED (n or
+ * c >= 2^31), SMC_ERR_CUDA.
+ */
+int smc_layer_norm(const void* x, const float* gamma, const float* beta, void* out, int64_t n,
+                   int64_t c, int dtype, float eps, smc_stream_t stream);
+
+/*
+ * Gradients of smc_layer_norm.  With xhat = (x - mean) / sqrt(var + eps) and
+ * g = grad_out * gamma:
+ *
+ *     grad_in    = (g - mean(g) - xhat * mean(g * xhat)) / sqrt(var + eps)
+ *     grad_gamma = sum over rows of grad_out * xhat
+ *     grad_beta  = sum over rows of grad_out
+ *
+ * The statistics are computed from x again, so the forward saves nothing.
+ *
+ * x, grad_out, grad_in  : device pointers, [n][c] of dtype.
+ * gamma                 : device pointer, float32 [c], or NULL (ones).
+ * grad_gamma, grad_beta : device pointers, float32 [c], or both NULL (not
+ *                         wanted); every element is overwritten (zeros for
+ *                         n = 0).
+ * workspace             : device pointer to smc_layer_norm_backward_workspace
+ *                         bytes, not shared with a call that may run at the
+ *                         same time; it needs no initialisation.
+ * grad_gamma and grad_beta are summed in fp32 in a fixed order that depends
+ * on n, c, dtype and the GPU's number of SMs only, without atomics: the same
+ * call gives the same bits.  Asynchronous on stream.
+ * Errors: as smc_layer_norm; SMC_ERR_INVALID also for a workspace that is too
+ * small, or outputs that overlap each other or an input.
+ */
+int smc_layer_norm_backward(const void* x, const float* gamma, const void* grad_out,
+                            void* grad_in, float* grad_gamma, float* grad_beta, int64_t n,
+                            int64_t c, int dtype, float eps, void* workspace,
+                            int64_t workspace_bytes, smc_stream_t stream);
+
+/* Bytes of workspace that smc_layer_norm_backward needs (0 possible), for the
+ * current device. */
+int smc_layer_norm_backward_workspace(int64_t n, int64_t c, int dtype, int64_t* bytes);
+
+/*
+ * Gated feed-forward product over the handle's rows: the first half of a
+ * gated SparseFeedForwardNet (trellis_sparse_mlx README, "What's in it"), two
+ * per-row linear maps of the same input, the activation and the product in
+ * one pass:
+ *
+ *     out = act(feats @ W[0] + bias[0]) * (feats @ W[1] + bias[1])
+ *
+ * The second half, the projection back to cin channels, is smc_forward_ex
+ * with K = 1 (bias, residual).  Like the K = 1 convolution this ignores the
+ * neighbour map; the handle supplies n and the device status word.
+ *
+ * feats  : device pointer, [n][cin] of dtype.
+ * W      : device pointer, [2][cin][hidden] of dtype: gate, then up.
+ * bias   : device pointer, [2][hidden] of dtype, or NULL.
+ * out    : device pointer, [n][hidden] of dtype; every element is overwritten.
+ * activation : enum smc_activation, of the gate (SMC_ACT_NONE: a bilinear
+ *          product).
+ * cin, hidden : any value from 1 to 65536.
+ * workspace   : device pointer to smc_gated_workspace bytes (16-byte aligned;
+ *          may be NULL when that is 0), not shared with a call that may run
+ *          at the same time; it needs no initialisation.
+ * Products are accumulated in fp32; bias, activation and product are applied
+ * to the accumulators and the result is rounded once to dtype.
+ * Asynchronous on stream, never synchronises; calls on one handle may run on
+ * different streams at once (each with its own workspace).
+ * Errors: as smc_forward; SMC_ERR_INVALID also for a bad activation, a
+ * workspace that is too small, or an output that overlaps an input.  A
+ * device-side wait that gives up is reported later by smc_device_status.
+ */
+int smc_gated_forward(smc_handle_t h, const void* feats, const void* W, const void* bias,
+                      void* out, int cin, int hidden, int dtype, int activation, void* workspace,
+                      int64_t workspace_bytes, smc_stream_t stream);
+
+/*
+ * Gradients of smc_gated_forward.  With g and u the two pre-activations
+ * (computed again from feats: the forward saves nothing):
+ *
+ *     dg = grad_out * u * act'(g)        du = grad_out * act(g)
+ *     grad_in   = dg @ W[0]^T + du @ W[1]^T
+ *     grad_W    = { feats^T @ dg, feats^T @ du }
+ *     grad_bias = { sum of dg over the rows, sum of du }
+ *
+ * feats, W, bias, activation, cin, hidden, workspace: as smc_gated_forward
+ *             (workspace of smc_gated_workspace bytes with backward != 0).
+ * grad_out  : device pointer, [n][hidden] of dtype.
+ * grad_in   : device pointer, [n][cin] of dtype, or NULL (not wanted).
+ * grad_W    : device pointer, [2][cin][hidden] of dtype, or NULL.
+ * grad_bias : device pointer, [2][hidden] of dtype, or NULL.
+ * Every element of the outputs that are given is overwritten (zeros in grad_W
+ * and grad_bias for n = 0).  dg and du are rounded to dtype between the
+ * products (SMC_F32: kept to fp32), all sums are fp32, each result is rounded
+ * once to dtype.  grad_W is in dtype, not fp32 as smc_backward_weight's: it
+ * carries the rounding of dg and du already.  relu'(0) = 0.  The sums over
+ * rows are split over CTAs and joined in a fixed order, without atomics: the
+ * same call gives the same bits.  Asynchronous on stream.
+ * Errors: as smc_gated_forward, outputs that overlap each other included.
+ */
+int smc_gated_backward(smc_handle_t h, const void* feats, const void* W, const void* bias,
+                       const void* grad_out, void* grad_in, void* grad_W, void* grad_bias, int cin,
+                       int hidden, int dtype, int activation, void* workspace,
+                       int64_t workspace_bytes, smc_stream_t stream);
+
+/* Bytes of workspace that smc_gated_forward (backward = 0) or
+ * smc_gated_backward (backward != 0) needs on this handle; 0 is possible. */
+int smc_gated_workspace(smc_handle_t h, int cin, int hidden, int dtype, int backward,
+                        int64_t* bytes);
+
+/*
+ * Dropout with the mask drawn from a counter-based generator, so that it is
+ * never stored, and the residual sum that closes a block:
+ *
+ *     out[i] = residual[i] + (bits(i) >= t ? x[i] * 65536 / (65536 - t) : 0)
+ *
+ * with t = round(p * 65536) and bits(i) 16 random bits: the Philox-4x32-10
+ * generator (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy
+ * as 1, 2, 3", SC 2011) with the key (low, high 32 bits of seed) maps the
+ * counter (low, high 32 bits of i / 8, low, high 32 bits of offset) to four
+ * words, and element i takes half i % 8 of them, low half first.  p is thus
+ * rounded to a multiple of 2^-16, and the scale is that of the rounded p.
+ *
+ * The backward pass is the same call on the gradient (same p, seed, offset
+ * and count, residual = NULL): it draws the same mask again.  A dropped
+ * element gives exactly 0 whatever x holds (NaN and infinity included).
+ *
+ * x, residual, out : device pointers, `count` elements of dtype; residual may
+ *             be NULL; out may be x or residual itself.
+ * p         : 0 <= p <= 1 (p = 1 drops everything).
+ * seed, offset : the generator's key and the counter's upper half: one seed
+ *             per training run, one offset per call.
+ * state     : device pointer to two uint64 {seed, offset}, or NULL.  If given,
+ *             the kernel reads the key from state[0] in place of seed, and
+ *             adds state[1] to offset: a captured graph draws new masks at
+ *             each replay when the caller advances state[1] between them.
+ * Arithmetic is fp32, rounded once to dtype.  Asynchronous on stream.
+ * Errors: SMC_ERR_INVALID (null or misaligned pointers, count < 0, bad dtype
+ * or p, out overlapping an input in any other way), SMC_ERR_CUDA.
+ */
+int smc_dropout(const void* x, const void* residual, void* out, int64_t count, int dtype, double p,
+                uint64_t seed, uint64_t offset, const uint64_t* state, smc_stream_t stream);
+
 /* Copy the int32 [n][27] neighbour map (-1 = no active neighbour) into
  * map_dev, asynchronously on stream.  Entry [i][k] is the row j whose
  * coordinates are coords[i] + stride * d(k) in the same batch: the indice map

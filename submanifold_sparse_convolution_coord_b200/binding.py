@@ -34,6 +34,8 @@ EXPORTS = (
     "smc_destroy", "smc_status_string", "smc_version", "smc_build_neighbor_map_static",
     "smc_backward_input", "smc_backward_weight", "smc_downsample2", "smc_subdivide2",
     "smc_forward_ex", "smc_autotune", "smc_conv_config_name", "smc_autotune_ex", "smc_replan",
+    "smc_layer_norm", "smc_layer_norm_backward", "smc_layer_norm_backward_workspace",
+    "smc_gated_forward", "smc_gated_backward", "smc_gated_workspace", "smc_dropout",
 )
 
 
@@ -93,6 +95,14 @@ def lib() -> ctypes.CDLL:
     L.smc_autotune_ex.argtypes = [p, p, p, p, i, i, i, i, i, p, ctypes.POINTER(i),
                                   ctypes.POINTER(i)]
     L.smc_replan.argtypes = [p, i, p]
+    f, u64 = ctypes.c_float, ctypes.c_uint64
+    L.smc_layer_norm.argtypes = [p, p, p, p, i64, i64, i, f, p]
+    L.smc_layer_norm_backward.argtypes = [p, p, p, p, p, p, i64, i64, i, f, p, i64, p]
+    L.smc_layer_norm_backward_workspace.argtypes = [i64, i64, i, ctypes.POINTER(i64)]
+    L.smc_gated_forward.argtypes = [p, p, p, p, p, i, i, i, i, p, i64, p]
+    L.smc_gated_backward.argtypes = [p, p, p, p, p, p, p, p, i, i, i, i, p, i64, p]
+    L.smc_gated_workspace.argtypes = [p, i, i, i, i, ctypes.POINTER(i64)]
+    L.smc_dropout.argtypes = [p, p, p, i64, i, ctypes.c_double, u64, u64, p, p]
     L.smc_conv_config_name.argtypes = [i]
     L.smc_conv_config_name.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -125,6 +135,65 @@ def _dev_ptr(t: torch.Tensor, name: str, dtype=None) -> int:
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
+
+
+class _Call:
+    """The device and stream of one row-operator call: `with _Call(x, stream) as c`
+    makes x's device current; c.empty() allocates results and workspaces on the
+    call's stream, and with an explicit stream c.keep() tells the allocator that
+    the call reads a tensor there, so that its memory is not reused too early."""
+
+    def __init__(self, x: torch.Tensor, stream: Optional[torch.cuda.Stream]):
+        self.device, self.stream = x.device, stream
+        if stream is not None and stream.device != x.device:
+            raise ValueError("stream must be on the tensors' device")
+        self.contexts = [torch.cuda.device(x.device)]
+        if stream is not None:
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def pointer(self) -> int:
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def keep(self, *tensors) -> None:
+        if self.stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _operand(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape,
+             dtype: Optional[torch.dtype] = None) -> Optional[int]:
+    """Device pointer of a tensor of this shape, on `like`'s device and in
+    `like`'s dtype unless another is given; None for None."""
+    if t is None:
+        return None
+    ptr = _dev_ptr(t, name, like.dtype if dtype is None else dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    return ptr
+
+
+def _rows(x: torch.Tensor, name: str) -> int:
+    """dtype code of an [N, C] feature matrix."""
+    if x.dim() != 2 or x.shape[1] < 1:
+        raise ValueError(f"{name} must be [N, C] with C >= 1")
+    if x.dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    return DTYPE_CODE[x.dtype]
 
 
 # ----------------------------------------------------------------------------
@@ -316,6 +385,149 @@ def smc_subdivide2(coords: torch.Tensor, feats: torch.Tensor,
     return out_c[:8 * n], out_f[:8 * n]
 
 
+def smc_layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+                   beta: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   out: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Layer norm of each row of x [N, C]; gamma and beta are float32 [C] or
+    None.  out may be x itself."""
+    code = _rows(x, "x")
+    n, c = x.shape
+    xp = _dev_ptr(x, "x")
+    gp = _operand(gamma, "gamma", x, (c,), torch.float32)
+    bp = _operand(beta, "beta", x, (c,), torch.float32)
+    with _Call(x, stream) as call:
+        if out is None:
+            out = call.empty((n, c), x.dtype)
+        op = _operand(out, "out", x, (n, c))
+        _check(lib().smc_layer_norm(xp, gp, bp, op, n, c, code, float(eps), call.pointer()),
+               "smc_layer_norm")
+        call.keep(x, gamma, beta, out)
+    return out
+
+
+def smc_layer_norm_backward_workspace(n: int, c: int, dtype: torch.dtype) -> int:
+    b = ctypes.c_int64(0)
+    _check(lib().smc_layer_norm_backward_workspace(n, c, DTYPE_CODE[dtype], ctypes.byref(b)),
+           "smc_layer_norm_backward_workspace")
+    return b.value
+
+
+def smc_layer_norm_backward(x: torch.Tensor, gamma: Optional[torch.Tensor],
+                            grad_out: torch.Tensor, eps: float = 1e-5,
+                            grad_in: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> tuple:
+    """Gradients of smc_layer_norm: (grad_in [N, C], grad_gamma, grad_beta
+    float32 [C]); the last two are None when gamma is None."""
+    code = _rows(x, "x")
+    n, c = x.shape
+    xp = _dev_ptr(x, "x")
+    gp = _operand(gamma, "gamma", x, (c,), torch.float32)
+    yp = _operand(grad_out, "grad_out", x, (n, c))
+    with _Call(x, stream) as call:
+        if grad_in is None:
+            grad_in = call.empty((n, c), x.dtype)
+        ip = _operand(grad_in, "grad_in", x, (n, c))
+        dgamma = dbeta = None
+        if gamma is not None:
+            dgamma, dbeta = call.empty((c,), torch.float32), call.empty((c,), torch.float32)
+        size = smc_layer_norm_backward_workspace(n, c, x.dtype)
+        work = call.empty((size,), torch.uint8)
+        _check(lib().smc_layer_norm_backward(
+            xp, gp, yp, ip, None if dgamma is None else dgamma.data_ptr(),
+            None if dbeta is None else dbeta.data_ptr(), n, c, code, float(eps), work.data_ptr(),
+            size, call.pointer()), "smc_layer_norm_backward")
+        call.keep(x, gamma, grad_out, grad_in)
+    return grad_in, dgamma, dbeta
+
+
+def smc_gated_workspace(handle: int, cin: int, hidden: int, dtype: torch.dtype,
+                        backward: bool) -> int:
+    b = ctypes.c_int64(0)
+    _check(lib().smc_gated_workspace(handle, int(cin), int(hidden), DTYPE_CODE[dtype],
+                                     int(bool(backward)), ctypes.byref(b)), "smc_gated_workspace")
+    return b.value
+
+
+def _handle_rows(handle: int, feats: torch.Tensor) -> int:
+    """The handle's number of rows, which feats must have."""
+    n = smc_get_sizes(handle)[0]
+    if feats.dim() != 2 or feats.shape[0] != n:
+        raise ValueError(f"feats must have the handle's {n} rows")
+    return n
+
+
+def smc_gated_forward(handle: int, feats: torch.Tensor, W: torch.Tensor, out: torch.Tensor,
+                      cin: int, hidden: int, bias: Optional[torch.Tensor] = None,
+                      activation: str = "silu",
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """out = act(feats @ W[0] + bias[0]) * (feats @ W[1] + bias[1])."""
+    code = _rows(feats, "feats")
+    n = _handle_rows(handle, feats)
+    fp = _operand(feats, "feats", feats, (n, cin))
+    wp = _operand(W, "W", feats, (2, cin, hidden))
+    bp = _operand(bias, "bias", feats, (2, hidden))
+    op = _operand(out, "out", feats, (n, hidden))
+    with _Call(feats, stream) as call:
+        size = smc_gated_workspace(handle, cin, hidden, feats.dtype, False)
+        work = call.empty((size,), torch.uint8) if size else None
+        _check(lib().smc_gated_forward(handle, fp, wp, bp, op, int(cin), int(hidden), code,
+                                       ACT_CODE[activation], work.data_ptr() if size else None,
+                                       size, call.pointer()), "smc_gated_forward")
+        call.keep(feats, W, bias, out)
+
+
+def smc_gated_backward(handle: int, feats: torch.Tensor, W: torch.Tensor, grad_out: torch.Tensor,
+                       grad_in: Optional[torch.Tensor], grad_W: Optional[torch.Tensor],
+                       grad_bias: Optional[torch.Tensor], cin: int, hidden: int,
+                       bias: Optional[torch.Tensor] = None, activation: str = "silu",
+                       stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Gradients of smc_gated_forward into those of grad_in, grad_W and
+    grad_bias that are not None."""
+    code = _rows(feats, "feats")
+    n = _handle_rows(handle, feats)
+    fp = _operand(feats, "feats", feats, (n, cin))
+    wp = _operand(W, "W", feats, (2, cin, hidden))
+    bp = _operand(bias, "bias", feats, (2, hidden))
+    yp = _operand(grad_out, "grad_out", feats, (n, hidden))
+    ip = _operand(grad_in, "grad_in", feats, (n, cin))
+    dwp = _operand(grad_W, "grad_W", feats, (2, cin, hidden))
+    dbp = _operand(grad_bias, "grad_bias", feats, (2, hidden))
+    with _Call(feats, stream) as call:
+        size = smc_gated_workspace(handle, cin, hidden, feats.dtype, True)
+        work = call.empty((size,), torch.uint8) if size else None
+        _check(lib().smc_gated_backward(handle, fp, wp, bp, yp, ip, dwp, dbp, int(cin),
+                                        int(hidden), code, ACT_CODE[activation],
+                                        work.data_ptr() if size else None, size, call.pointer()),
+               "smc_gated_backward")
+        call.keep(feats, W, bias, grad_out, grad_in, grad_W, grad_bias)
+
+
+def smc_dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
+                residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                state: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """residual + dropout(x), the mask drawn from (seed, offset); the backward
+    pass is smc_dropout(grad, p, seed, offset).  state: CUDA int64 [2], read on
+    the device: its seed in place of seed, and its offset added to offset.  out
+    may be x or residual itself."""
+    if x.dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset must be in [0, 2^64)")
+    xp = _dev_ptr(x, "x")
+    rp = _operand(residual, "residual", x, x.shape)
+    sp = _operand(state, "state", x, (2,), torch.int64)
+    with _Call(x, stream) as call:
+        if out is None:
+            out = call.empty(x.shape, x.dtype)
+        op = _operand(out, "out", x, x.shape)
+        _check(lib().smc_dropout(xp, rp, op, x.numel(), DTYPE_CODE[x.dtype], float(p), seed, offset,
+                                 sp, call.pointer()), "smc_dropout")
+        call.keep(x, residual, state, out)
+    return out
+
+
 def smc_get_neighbor_map(handle: int, map_out: torch.Tensor,
                          stream: Optional[torch.cuda.Stream] = None) -> None:
     rc = lib().smc_get_neighbor_map(ctypes.c_void_p(handle),
@@ -470,6 +682,36 @@ class SubMIndex:
             out = torch.empty((K ** 3, cin, cout), dtype=torch.float32, device=feats.device)
         smc_backward_weight(self.handle, feats, grad_out, out, K, cin, cout)
         return out
+
+
+    def gated_forward(self, feats: torch.Tensor, W: torch.Tensor,
+                      bias: Optional[torch.Tensor] = None, activation: str = "silu",
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """act(feats @ W[0] + bias[0]) * (feats @ W[1] + bias[1]), [N, hidden]
+        for W [2, Cin, hidden] and bias [2, hidden]."""
+        cin, hidden = self._gated_shape(feats, W)
+        if out is None:
+            out = torch.empty((self.n, hidden), dtype=feats.dtype, device=feats.device)
+        smc_gated_forward(self.handle, feats, W, out, cin, hidden, bias, activation)
+        return out
+
+    def gated_backward(self, feats: torch.Tensor, W: torch.Tensor, grad_out: torch.Tensor,
+                       bias: Optional[torch.Tensor] = None, activation: str = "silu") -> tuple:
+        """Gradients of gated_forward: (grad_in [N, Cin], grad_W [2, Cin,
+        hidden], grad_bias [2, hidden] or None without bias), in feats' dtype."""
+        cin, hidden = self._gated_shape(feats, W)
+        grad_in, grad_W = torch.empty_like(feats), torch.empty_like(W)
+        grad_bias = None if bias is None else torch.empty_like(bias)
+        smc_gated_backward(self.handle, feats, W, grad_out, grad_in, grad_W, grad_bias, cin,
+                           hidden, bias, activation)
+        return grad_in, grad_W, grad_bias
+
+    def _gated_shape(self, feats: torch.Tensor, W: torch.Tensor) -> tuple:
+        if feats.dim() != 2 or feats.shape[0] != self.n:
+            raise ValueError("feats must be [N, Cin] for this index")
+        if W.dim() != 3 or W.shape[0] != 2 or W.shape[1] != feats.shape[1]:
+            raise ValueError("W must be [2, Cin, hidden]")
+        return W.shape[1], W.shape[2]
 
 
 def submconv3d(index: SubMIndex, feats: torch.Tensor, W: torch.Tensor, K: int = 3,

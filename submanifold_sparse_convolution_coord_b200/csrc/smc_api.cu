@@ -44,6 +44,28 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether two buffers share a byte (null buffers share none).
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + uintptr_t(b.bytes) && y < x + uintptr_t(a.bytes);
+}
+// Whether one of the outputs overlaps another output or an input.
+template <int NO, int NI>
+bool any_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+    for (int j = 0; j < NI; ++j)
+      if (overlap(outs[i], ins[j])) return true;
+  }
+  return false;
+}
+
 int elem_bytes(int dtype) {
   switch (dtype) {
     case SMC_F32:
@@ -370,6 +392,155 @@ int smc_subdivide2(const int32_t* coords_dev, int64_t n, const void* feats_dev, 
   if (n >= (int64_t(1) << 28)) return SMC_ERR_UNSUPPORTED;
   return smc::subdivide2(coords_dev, n, feats_dev, c, dtype, out_coords_dev, out_feats_dev,
                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+int check_norm(int64_t n, int64_t c, int dtype, float eps) {
+  if (n < 0 || c < 1 || elem_bytes(dtype) == 0 || !(eps >= 0.f)) return SMC_ERR_INVALID;
+  if (n >= (int64_t(1) << 31) || c >= (int64_t(1) << 31)) return SMC_ERR_UNSUPPORTED;
+  // no buffer of a real device comes near: byte counts stay inside int64
+  if (c > 0 && n > (int64_t(1) << 44) / c) return SMC_ERR_UNSUPPORTED;
+  return SMC_OK;
+}
+
+constexpr int kMaxGatedChannels = 65536;
+
+int check_gated(smc_handle_t h, int cin, int hidden, int dtype) {
+  const int rc = check_call(h, 1, cin, hidden, dtype);
+  if (rc != SMC_OK) return rc;
+  return cin > kMaxGatedChannels || hidden > kMaxGatedChannels ? SMC_ERR_INVALID : SMC_OK;
+}
+
+}  // namespace
+
+int smc_layer_norm(const void* x, const float* gamma, const float* beta, void* out, int64_t n,
+                   int64_t c, int dtype, float eps, smc_stream_t stream) {
+  const int rc = check_norm(n, c, dtype, eps);
+  if (rc != SMC_OK) return rc;
+  if (!aligned16(gamma) || !aligned16(beta)) return SMC_ERR_INVALID;
+  if (n == 0) return SMC_OK;
+  if (!x || !out || !aligned16(x) || !aligned16(out)) return SMC_ERR_INVALID;
+  const int64_t rows = n * c * elem_bytes(dtype);
+  const Span outs[] = {{out, rows}};
+  const Span ins[] = {{x == out ? nullptr : x, rows}, {gamma, c * 4}, {beta, c * 4}};
+  if (any_overlap(outs, ins)) return SMC_ERR_INVALID;
+  return smc::layer_norm(x, gamma, beta, out, n, c, dtype, eps,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+int smc_layer_norm_backward_workspace(int64_t n, int64_t c, int dtype, int64_t* bytes) {
+  if (!bytes) return SMC_ERR_INVALID;
+  *bytes = 0;
+  const int rc = check_norm(n, c, dtype, 0.f);
+  if (rc != SMC_OK) return rc;
+  *bytes = smc::layer_norm_backward_workspace(n, c, dtype);
+  return SMC_OK;
+}
+
+int smc_layer_norm_backward(const void* x, const float* gamma, const void* grad_out,
+                            void* grad_in, float* grad_gamma, float* grad_beta, int64_t n,
+                            int64_t c, int dtype, float eps, void* workspace,
+                            int64_t workspace_bytes, smc_stream_t stream) {
+  const int rc = check_norm(n, c, dtype, eps);
+  if (rc != SMC_OK) return rc;
+  if (!aligned16(gamma) || !aligned16(grad_gamma) || !aligned16(grad_beta)) return SMC_ERR_INVALID;
+  if ((grad_gamma == nullptr) != (grad_beta == nullptr)) return SMC_ERR_INVALID;
+  if (n > 0 && (!x || !grad_out || !grad_in || !aligned16(x) || !aligned16(grad_out) ||
+                !aligned16(grad_in)))
+    return SMC_ERR_INVALID;
+  const int64_t need = smc::layer_norm_backward_workspace(n, c, dtype);
+  if (workspace_bytes < need || (need > 0 && !workspace) || !aligned16(workspace))
+    return SMC_ERR_INVALID;
+  const int64_t rows = n * c * elem_bytes(dtype);
+  const Span outs[] = {{grad_in, rows}, {grad_gamma, c * 4}, {grad_beta, c * 4}, {workspace, need}};
+  const Span ins[] = {{x, rows}, {grad_out, rows}, {gamma, c * 4}};
+  if (any_overlap(outs, ins)) return SMC_ERR_INVALID;
+  return smc::layer_norm_backward(x, gamma, grad_out, grad_in, grad_gamma, grad_beta, n, c, dtype,
+                                  eps, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int smc_gated_workspace(smc_handle_t h, int cin, int hidden, int dtype, int backward,
+                        int64_t* bytes) {
+  if (!bytes) return SMC_ERR_INVALID;
+  *bytes = 0;
+  const int rc = check_gated(h, cin, hidden, dtype);
+  if (rc != SMC_OK) return rc;
+  *bytes = smc::gated_workspace(h->plan.n, cin, hidden, dtype, backward != 0);
+  return SMC_OK;
+}
+
+int smc_gated_forward(smc_handle_t h, const void* feats, const void* W, const void* bias,
+                      void* out, int cin, int hidden, int dtype, int activation, void* workspace,
+                      int64_t workspace_bytes, smc_stream_t stream) {
+  const int rc = check_gated(h, cin, hidden, dtype);
+  if (rc != SMC_OK) return rc;
+  if (activation < SMC_ACT_NONE || activation > SMC_ACT_GELU) return SMC_ERR_INVALID;
+  const int64_t n = h->plan.n, e = elem_bytes(dtype);
+  if (n == 0) return SMC_OK;
+  if (!feats || !W || !out) return SMC_ERR_INVALID;
+  if (!aligned16(feats) || !aligned16(W) || !aligned16(out) || !aligned16(bias))
+    return SMC_ERR_INVALID;
+  const int64_t need = smc::gated_workspace(n, cin, hidden, dtype, false);
+  if (workspace_bytes < need || (need > 0 && !workspace) || !aligned16(workspace))
+    return SMC_ERR_INVALID;
+  const Span outs[] = {{out, n * hidden * e}, {workspace, need}};
+  const Span ins[] = {{feats, n * cin * e}, {W, 2 * e * cin * hidden}, {bias, 2 * e * hidden}};
+  if (any_overlap(outs, ins)) return SMC_ERR_INVALID;
+  const smc::GatedCall g{feats, W, bias, n, cin, hidden, dtype, activation, workspace,
+                         h->plan.status};
+  return smc::gated_forward(g, out, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int smc_gated_backward(smc_handle_t h, const void* feats, const void* W, const void* bias,
+                       const void* grad_out, void* grad_in, void* grad_W, void* grad_bias, int cin,
+                       int hidden, int dtype, int activation, void* workspace,
+                       int64_t workspace_bytes, smc_stream_t stream) {
+  const int rc = check_gated(h, cin, hidden, dtype);
+  if (rc != SMC_OK) return rc;
+  if (activation < SMC_ACT_NONE || activation > SMC_ACT_GELU) return SMC_ERR_INVALID;
+  const int64_t n = h->plan.n, e = elem_bytes(dtype);
+  const int64_t w_bytes = 2 * e * cin * hidden, b_bytes = 2 * e * hidden;
+  if (!W || !aligned16(W) || !aligned16(bias) || !aligned16(grad_in) || !aligned16(grad_W) ||
+      !aligned16(grad_bias))
+    return SMC_ERR_INVALID;
+  if (n > 0 && (!feats || !grad_out || !aligned16(feats) || !aligned16(grad_out)))
+    return SMC_ERR_INVALID;
+  const int64_t need = smc::gated_workspace(n, cin, hidden, dtype, true);
+  if (workspace_bytes < need || (need > 0 && !workspace) || !aligned16(workspace))
+    return SMC_ERR_INVALID;
+  const Span outs[] = {{grad_in, n * cin * e}, {grad_W, w_bytes}, {grad_bias, b_bytes},
+                       {workspace, need}};
+  const Span ins[] = {{feats, n * cin * e}, {W, w_bytes}, {bias, b_bytes},
+                      {grad_out, n * hidden * e}};
+  if (any_overlap(outs, ins)) return SMC_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (n == 0) {
+    if ((grad_W && cudaMemsetAsync(grad_W, 0, size_t(w_bytes), s) != cudaSuccess) ||
+        (grad_bias && cudaMemsetAsync(grad_bias, 0, size_t(b_bytes), s) != cudaSuccess))
+      return SMC_ERR_CUDA;
+    return SMC_OK;
+  }
+  const smc::GatedCall g{feats, W, bias, n, cin, hidden, dtype, activation, workspace,
+                         h->plan.status};
+  return smc::gated_backward(g, grad_out, grad_in, grad_W, grad_bias, s);
+}
+
+int smc_dropout(const void* x, const void* residual, void* out, int64_t count, int dtype, double p,
+                uint64_t seed, uint64_t offset, const uint64_t* state, smc_stream_t stream) {
+  if (count < 0 || elem_bytes(dtype) == 0 || !(p >= 0.0 && p <= 1.0)) return SMC_ERR_INVALID;
+  if (count >= (int64_t(1) << 44)) return SMC_ERR_INVALID;
+  if (!aligned16(state)) return SMC_ERR_INVALID;
+  if (count == 0) return SMC_OK;
+  if (!x || !out || !aligned16(x) || !aligned16(out) || !aligned16(residual))
+    return SMC_ERR_INVALID;
+  const int64_t bytes = count * elem_bytes(dtype);
+  const Span outs[] = {{out, bytes}};
+  const Span ins[] = {{x == out ? nullptr : x, bytes}, {residual == out ? nullptr : residual, bytes},
+                      {state, 16}};
+  if (any_overlap(outs, ins)) return SMC_ERR_INVALID;
+  return smc::dropout(x, residual, out, count, dtype, p, seed, offset, state,
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
 int smc_get_neighbor_map(smc_handle_t h, int32_t* map_dev, smc_stream_t stream) {

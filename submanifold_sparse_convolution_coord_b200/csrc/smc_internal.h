@@ -139,6 +139,33 @@ int downsample2(const int32_t* coords, int64_t n, const void* feats, int c, int 
 int subdivide2(const int32_t* coords, int64_t n, const void* feats, int c, int dtype,
                int32_t* out_coords, void* out_feats, cudaStream_t s);
 
+// Layer norm (smc_norm.cu).
+int layer_norm(const void* x, const float* gamma, const float* beta, void* out, int64_t n,
+               int64_t c, int dtype, float eps, cudaStream_t s);
+int64_t layer_norm_backward_workspace(int64_t n, int64_t c, int dtype);
+int layer_norm_backward(const void* x, const float* gamma, const void* dy, void* dx,
+                        float* dgamma, float* dbeta, int64_t n, int64_t c, int dtype, float eps,
+                        void* workspace, cudaStream_t s);
+
+// Gated feed-forward product (smc_gated.cu).
+struct GatedCall {
+  const void* x;     // [n][cin]
+  const void* W;     // [2][cin][hidden]
+  const void* bias;  // [2][hidden] or null
+  int64_t n;
+  int cin, hidden, dtype, act;
+  void* workspace;
+  int32_t* status;  // device status word of the handle
+};
+int64_t gated_workspace(int64_t n, int cin, int hidden, int dtype, bool backward);
+int gated_forward(const GatedCall& g, void* out, cudaStream_t s);
+int gated_backward(const GatedCall& g, const void* dh, void* dx, void* dW, void* dbias,
+                   cudaStream_t s);
+
+// Dropout (smc_dropout.cu).
+int dropout(const void* x, const void* residual, void* out, int64_t count, int dtype, double p,
+            uint64_t seed, uint64_t offset, const uint64_t* state, cudaStream_t s);
+
 // CUDA-core convolution (smc_conv_simt.cu): any cin, cout, dtype.
 int launch_conv_simt(const Plan& plan, bool dense, const void* feats, const void* W, void* out,
                      int cin, int cout, int dtype, const Epilogue& ep, cudaStream_t stream);
