@@ -43,10 +43,13 @@ using namespace ptx;
 enum Mode { kPre, kPreBwd, kDx, kDw };
 
 constexpr int kBK = 64;  // depth of a stage: one 128-byte row of 16-bit values
-constexpr int kThreads = 384;
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8;  // two per quarter of the tensor-memory lanes
+// Sixteen epilogue warps, four per quarter of the tensor-memory lanes: a warp's
+// way through a chunk is a chain of latencies (accumulator load, exponential,
+// division, staging, fence), so each scheduler gets four of them to interleave
+// (55,100 rows, 512 -> 2048 bf16, SiLU: TODO us with eight, TODO us with sixteen).
+constexpr int kEpiWarp0 = 4, kEpiWarps = 16;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kSmemMax = 227 * 1024;
-constexpr int kTailBytes = 4096;  // bias (2 KB) and barriers
 constexpr uint64_t kAbortDrainNs = 50000000ull;
 
 // The part products of fp32 inputs, smallest first: parts of A and of B.
@@ -103,8 +106,13 @@ struct Walk {
       g.k0 = int(cur % a.k_iters);
       g.k1 = int(min(int64_t(a.k_iters), g.k0 + end - cur));
       cur += g.k1 - g.k0;
-      g.s = tile / (a.n_tiles * a.m_tiles);
-      tile -= g.s * a.n_tiles * a.m_tiles;
+      // channel tiles outermost: pairs half the launch apart then read the
+      // same rows of dg and du at the same time, from L2
+      g.n = tile / (2 * a.m_tiles);
+      tile -= g.n * 2 * a.m_tiles;
+      g.s = tile / a.m_tiles;
+      g.m = tile % a.m_tiles;
+      return true;
     } else {
       tile = int(cur);
       g.k0 = 0;
@@ -123,34 +131,44 @@ struct Walk {
 // rounding; exp(-v) = inf gives the correct limit 0).
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
-__device__ __forceinline__ float act_value(float v, int act) {
-  switch (act) {
-    case SMC_ACT_RELU:
-      return fmaxf(v, 0.f);
-    case SMC_ACT_SILU:
-      return v * sigmoid(v);
-    case SMC_ACT_GELU:
-      return 0.5f * v * (1.f + erff(v * 0.7071067811865476f));
-    default:
-      return v;
-  }
+// The normal distribution function of v and exp(-v^2 / 2), for GELU and its
+// slope: erfc(x) = t (a1 + a2 t + ... + a5 t^4) exp(-x^2), t = 1 / (1 + p x),
+// x = |v| / sqrt(2) (Hastings, "Approximations for Digital Computers", 1955;
+// Abramowitz and Stegun 7.1.26: within 1.5e-7 of erfc, so within 1e-7 of the
+// function), one exponential and one division where erff takes two polynomials
+// (55,100 rows, 512 -> 2048 bf16: 281 us with erff, TODO us with this).
+__device__ __forceinline__ float2 normal_cdf(float v) {
+  const float e = __expf(-0.5f * v * v);
+  const float t = __fdividef(1.f, fmaf(0.3275911f * 0.7071067811865476f, fabsf(v), 1.f));
+  float q = fmaf(t, 1.061405429f, -1.453152027f);
+  q = fmaf(t, q, 1.421413741f);
+  q = fmaf(t, q, -0.284496736f);
+  q = fmaf(t, q, 0.254829592f);
+  q *= 0.5f * t * e;
+  return make_float2(v > 0.f ? 1.f - q : q, e);
 }
-// The activation's value and slope.
-__device__ __forceinline__ float2 act_both(float v, int act) {
-  switch (act) {
-    case SMC_ACT_RELU:
-      return make_float2(fmaxf(v, 0.f), v > 0.f ? 1.f : 0.f);
-    case SMC_ACT_SILU: {
-      const float s = sigmoid(v);
-      return make_float2(v * s, s * (1.f + v * (1.f - s)));
-    }
-    case SMC_ACT_GELU: {
-      const float cdf = 0.5f * (1.f + erff(v * 0.7071067811865476f));
-      return make_float2(v * cdf, cdf + v * __expf(-0.5f * v * v) * 0.3989422804014327f);
-    }
-    default:
-      return make_float2(v, 1.f);
+
+// The activation's value, and its value and slope.  ACT is a template parameter
+// so that the exponentials of many elements are in flight at once.
+template <int ACT>
+__device__ __forceinline__ float act_value(float v) {
+  if constexpr (ACT == SMC_ACT_RELU) return fmaxf(v, 0.f);
+  if constexpr (ACT == SMC_ACT_SILU) return v * sigmoid(v);
+  if constexpr (ACT == SMC_ACT_GELU) return v * normal_cdf(v).x;
+  return v;
+}
+template <int ACT>
+__device__ __forceinline__ float2 act_both(float v) {
+  if constexpr (ACT == SMC_ACT_RELU) return make_float2(fmaxf(v, 0.f), v > 0.f ? 1.f : 0.f);
+  if constexpr (ACT == SMC_ACT_SILU) {
+    const float s = sigmoid(v);
+    return make_float2(v * s, s * (1.f + v * (1.f - s)));
   }
+  if constexpr (ACT == SMC_ACT_GELU) {
+    const float2 c = normal_cdf(v);
+    return make_float2(v * c.x, c.x + v * c.y * 0.3989422804014327f);
+  }
+  return make_float2(v, 1.f);
 }
 
 // x = p[0] + p[1] + p[2] exactly (to 24 bits), each part a bf16 value.  A value
@@ -187,13 +205,17 @@ struct Smem {
   static constexpr int kB = BN / 2 * 128;  // this CTA's half of B
   static constexpr int kStage = 16384 + kB;
   static constexpr int kChunkBytes = DT == SMC_F32 ? 4096 : 2048;  // 32 rows x 32 values
-  static constexpr int kChunks = MODE == kPre || MODE == kPreBwd ? BN / 128 : BN / 64;
-  // kPreBwd: dh of every chunk (dg takes its place) and du of every chunk (of
-  // one for fp32, whose du is staged for its column sums only); kPre, kDx: two
-  // slots in turn; kDw stores straight from registers.
-  static constexpr int kWarpStage =
-      MODE == kPreBwd ? (kChunks + (DT == SMC_F32 ? 1 : kChunks)) * kChunkBytes
-                      : (MODE == kDw ? 0 : 2 * kChunkBytes);
+  // chunks of a tile's outputs, dealt to four warps per lane quarter
+  static constexpr int kTileChunks = MODE == kPre || MODE == kPreBwd ? BN / 64 : BN / 32;
+  static constexpr int kChunks = (kTileChunks + 3) / 4;  // per warp
+  // kPreBwd: dh of this tile (dg takes its place) and of the next, and du;
+  // fp32, whose tiles take six times the products, reads dh and writes the
+  // parts of dg and du directly.  kPre, kDx: the outgoing chunk.  kDw stores
+  // from registers.
+  static constexpr int kSlots = MODE == kDw ? 0 : (MODE == kPreBwd ? (DT == SMC_F32 ? 0 : 3) : 1);
+  static constexpr int kWarpStage = kSlots * kChunkBytes;
+  static constexpr int kBias = 64 * (DT == SMC_F32 ? 4 : 2);  // bias of a warp's chunk
+  static constexpr int kTailBytes = kEpiWarps * kBias + 512;  // and the barriers
   static constexpr int kStages0 = (kSmemMax - kTailBytes - kEpiWarps * kWarpStage) / kStage;
   static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
   static constexpr int kBytes = kStages * kStage + kEpiWarps * kWarpStage + kTailBytes;
@@ -276,15 +298,180 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* map, bool tma, ui
   }
 }
 
-// Sum over a staged chunk's 32 rows, for column `lane`.
+// Sum over a staged 16-bit chunk's 32 rows, for column `lane`: half a warp
+// takes the even rows and half the odd ones, two columns a lane.
 template <int DT>
 __device__ __forceinline__ float column_sum(const uint8_t* chunk, int lane) {
   using T = typename Elem<DT>::type;
-  float s = 0.f;
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r)
-    s += rows::to_float(*reinterpret_cast<const T*>(chunk + value_at<DT>(r, lane)));
-  return s;
+  float s0 = 0.f, s1 = 0.f;
+  const int col = (lane & 15) * 2;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    uint32_t w = *reinterpret_cast<const uint32_t*>(chunk + value_at<DT>(2 * i + (lane >> 4), col));
+    const T* t = reinterpret_cast<const T*>(&w);
+    s0 += rows::to_float(t[0]);
+    s1 += rows::to_float(t[1]);
+  }
+  s0 += __shfl_xor_sync(0xffffffffu, s0, 16);
+  s1 += __shfl_xor_sync(0xffffffffu, s1, 16);
+  // column `lane` is in lane lane / 2
+  const float a = __shfl_sync(0xffffffffu, s0, lane >> 1);
+  const float b = __shfl_sync(0xffffffffu, s1, lane >> 1);
+  return lane & 1 ? b : a;
+}
+
+// Sums over the warp's lanes of eight values each; lane l ends with the sum of
+// value l / 4 (exchanges that halve the values three times, then two plain steps).
+__device__ __forceinline__ float sum8(const float (&v)[8], int lane) {
+  float a[4], b[2], c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool up = lane & 16;
+    const float send = up ? v[i] : v[i + 4], keep = up ? v[i + 4] : v[i];
+    a[i] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 8;
+    const float send = up ? a[i] : a[i + 2], keep = up ? a[i + 2] : a[i];
+    b[i] = keep + __shfl_xor_sync(0xffffffffu, send, 8);
+  }
+  {
+    const bool up = lane & 4;
+    const float send = up ? b[0] : b[1], keep = up ? b[1] : b[0];
+    c = keep + __shfl_xor_sync(0xffffffffu, send, 4);
+  }
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  return c + __shfl_xor_sync(0xffffffffu, c, 1);
+}
+
+// What one lane needs for its row of a 32 x 32 chunk of g and u.
+struct GateRow {
+  const uint8_t* bias;  // [2][32] values in shared memory: of g, of u; or null
+  uint8_t *slot, *slot_u;
+  int lane;
+  bool row_ok;
+  const float* dh;  // fp32, kPreBwd: the row's dh (dh_vec: 16-byte aligned)
+  bool dh_vec;
+  uint16_t* dgu;  // fp32, kPreBwd: where the row's dg parts go
+  int Hp, valid;  // valid: columns of the chunk that exist
+  float* db;      // fp32, kPreBwd: the chunk's column sums of dg, or null
+  int64_t db_u;   // from there to those of du
+};
+
+// Columns g8 * 8 .. + 7 of it.  kPre: act(g) u into `slot`; kPreBwd: dh from
+// `slot`, dg in its place and du into `slot_u` (fp32: their parts to dgu).
+template <int MODE, int DT, int ACT, bool BIAS>
+__device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, int g8,
+                                      const GateRow& c) {
+  float gg[8], uu[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    gg[i] = __uint_as_float(gv[i]);
+    uu[i] = __uint_as_float(uv[i]);
+  }
+  if constexpr (BIAS) {
+    using T = typename Elem<DT>::type;
+    uint4 raw[2][sizeof(T) / 2];
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i) {
+      raw[0][i] = reinterpret_cast<const uint4*>(c.bias + g8 * 8 * sizeof(T))[i];
+      raw[1][i] = reinterpret_cast<const uint4*>(c.bias + (32 + g8 * 8) * sizeof(T))[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      gg[i] += rows::to_float(reinterpret_cast<const T*>(raw[0])[i]);
+      uu[i] += rows::to_float(reinterpret_cast<const T*>(raw[1])[i]);
+    }
+  }
+  if constexpr (MODE == kPre) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_value<ACT>(gg[i]) * uu[i];
+    put8<DT>(c.slot, c.lane, g8, v);
+  } else {
+    float dh[8], G[8], U[8];
+    if constexpr (DT != SMC_F32) {
+      get8<DT>(c.slot, c.lane, g8, dh);
+    } else {
+      const int left = c.row_ok ? c.valid - g8 * 8 : 0;
+      if (c.dh_vec && left >= 8) {
+        const float4 p = *reinterpret_cast<const float4*>(c.dh + g8 * 8);
+        const float4 q = *reinterpret_cast<const float4*>(c.dh + g8 * 8 + 4);
+        dh[0] = p.x, dh[1] = p.y, dh[2] = p.z, dh[3] = p.w;
+        dh[4] = q.x, dh[5] = q.y, dh[6] = q.z, dh[7] = q.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dh[i] = i < left ? c.dh[g8 * 8 + i] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = act_both<ACT>(gg[i]);
+      G[i] = dh[i] * uu[i] * f.y;  // dh is 0 in rows and columns that do not exist
+      U[i] = dh[i] * f.x;
+    }
+    if constexpr (DT != SMC_F32) {
+      put8<DT>(c.slot, c.lane, g8, G);
+      put8<DT>(c.slot_u, c.lane, g8, U);
+    } else {
+      if (c.db) {
+        const float sg = sum8(G, c.lane), su = sum8(U, c.lane);
+        const int col = g8 * 8 + (c.lane >> 2);
+        if ((c.lane & 3) == 0 && col < c.valid) {
+          c.db[col] = sg;
+          c.db[c.db_u + col] = su;
+        }
+      }
+      if (c.row_ok && g8 * 8 < c.valid) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          uint32_t w3[3][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            __nv_bfloat16 lo[3], hi[3];
+            split3(s ? U[2 * i] : G[2 * i], lo);
+            split3(s ? U[2 * i + 1] : G[2 * i + 1], hi);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+              w3[p][i] = uint32_t(__bfloat16_as_ushort(lo[p])) |
+                         uint32_t(__bfloat16_as_ushort(hi[p])) << 16;
+          }
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+            *reinterpret_cast<uint4*>(c.dgu + (p * 2 + s) * c.Hp + g8 * 8) =
+                make_uint4(w3[p][0], w3[p][1], w3[p][2], w3[p][3]);
+        }
+      }
+    }
+  }
+}
+
+// Sixteen columns (half `hf` of the chunk).  The activation and the presence of
+// a bias are chosen once here, so that the code of a choice is straight.
+template <int MODE, int DT>
+__device__ __forceinline__ void gate16(const uint32_t (&gv)[16], const uint32_t (&uv)[16], int hf,
+                                       int act, const GateRow& c) {
+  auto go = [&](auto a, auto b) {
+    gate8<MODE, DT, decltype(a)::value, decltype(b)::value>(gv, uv, 2 * hf, c);
+    gate8<MODE, DT, decltype(a)::value, decltype(b)::value>(gv + 8, uv + 8, 2 * hf + 1, c);
+  };
+  auto choose = [&](auto b) {
+    switch (act) {
+      case SMC_ACT_RELU:
+        return go(std::integral_constant<int, SMC_ACT_RELU>(), b);
+      case SMC_ACT_SILU:
+        return go(std::integral_constant<int, SMC_ACT_SILU>(), b);
+      case SMC_ACT_GELU:
+        return go(std::integral_constant<int, SMC_ACT_GELU>(), b);
+      default:
+        return go(std::integral_constant<int, SMC_ACT_NONE>(), b);
+    }
+  };
+  if (c.bias)
+    choose(std::true_type());
+  else
+    choose(std::false_type());
 }
 
 template <int MODE, int BN, int DT>
@@ -306,10 +493,12 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;
   uint8_t* staging = smem + kStages * L::kStage;
-  float* bias_smem = reinterpret_cast<float*>(staging + kEpiWarps * L::kWarpStage);  // [8][64]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(bias_smem + kEpiWarps * 64);
-  // full[kStages] empty[kStages] tfull[2] tempty[2] drain dh[8]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5 + kEpiWarps);
+  uint8_t* bias_smem = staging + kEpiWarps * L::kWarpStage;  // [kEpiWarps][kBias]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(bias_smem + kEpiWarps * L::kBias);
+  // full[kStages] empty[kStages] tfull[2] tempty[2] drain dh[kEpiWarps][2]
+  constexpr int kBars = 2 * kStages + 5 + 2 * kEpiWarps;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+  static_assert(kBars * 8 + 8 <= 512, "barriers");
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -330,7 +519,7 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
       mbar_init(tempty0 + 8 * i, 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
-    for (int w = 0; w < kEpiWarps; ++w) mbar_init(dh0 + 8 * w, 1);
+    for (int w = 0; w < 2 * kEpiWarps; ++w) mbar_init(dh0 + 8 * w, 1);
     *abort_flag = 0;
     mbar_init_fence_cluster();
     // the 128-byte swizzle needs the ring 1024-byte aligned
@@ -440,180 +629,143 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
     }
   } else if (warp >= kEpiWarp0) {
     // ---------------- epilogue -------------------------------------------------
-    const int quarter = warp & 3, half = (warp - kEpiWarp0) >> 2, w = warp - kEpiWarp0;
+    const int quarter = warp & 3, group = (warp - kEpiWarp0) >> 2, w = warp - kEpiWarp0;
     uint8_t* mine = staging + w * L::kWarpStage;
-    float* bias_w = bias_smem + w * 64;
+    T* bias_w = reinterpret_cast<T*>(bias_smem + w * L::kBias);
     const uint32_t lead_tempty0 = map_to_rank(tempty0, 0);
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
-    const uint32_t dh_bar = dh0 + 8 * w;
-    uint32_t dh_phase = 0;
-    int seg = 0, turn = 0;  // turn: the staging slot of the next store
+    const uint32_t dh_bar0 = dh0 + 16 * w;
+    const int hc = group * 32;  // kPre, kPreBwd: the warp's chunk of every tile
+    const int64_t my_rows = rank * 128 + quarter * 32;
+    int seg = 0;
+    uint32_t dh_phases = 0;  // the parity to wait for next, per slot
     bool ok = *abort_flag == 0;
-    while (ok && walk.next(g)) {
-      const int acc = seg & 1;
+
+    // What a tile's epilogue needs from memory, asked for one tile ahead: the
+    // bias of column `lane`, and dh into the staging.
+    T next_bias[2] = {};
+    auto live_of = [&](const Seg& t) {
+      return hc < BN / 2 && int64_t(t.m) * 256 + my_rows < a.n && t.n * (BN / 2) + hc < a.H;
+    };
+    auto prefetch = [&](const Seg& t, int slot) {
+      if (!kPreMode || !live_of(t)) return;
+      const int h = t.n * (BN / 2) + hc;
+      if (a.bias && h + lane < a.H) {
+        next_bias[0] = static_cast<const T*>(a.bias)[h + lane];
+        next_bias[1] = static_cast<const T*>(a.bias)[a.H + h + lane];
+      }
+      if constexpr (MODE == kPreBwd && DT != SMC_F32) {
+        const int64_t row0 = int64_t(t.m) * 256 + my_rows;
+        uint8_t* to = mine + slot * L::kChunkBytes;
+        if (a.tma_dh) {
+          fence_proxy_async_smem();  // all lanes have read and written the slot
+          __syncwarp();
+          if (lane == 0) {
+            bulk_wait_read<0>();
+            mbar_arrive_expect_tx(dh_bar0 + 8 * slot, L::kChunkBytes);
+            tma_load_3d(smem_addr(to), &map_dh, h, int(row0), 0, dh_bar0 + 8 * slot);
+          }
+        } else {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          const int rows_here = int(min(int64_t(32), a.n - row0));
+          const T* from = static_cast<const T*>(a.dh) + row0 * a.H + h + lane;
+#pragma unroll 8
+          for (int r = 0; r < 32; ++r)
+            *reinterpret_cast<T*>(to + value_at<DT>(r, lane)) =
+                r < rows_here && h + lane < a.H ? from[int64_t(r) * a.H]
+                                                : rows::from_float<T>(0.f);
+        }
+      }
+    };
+    Seg gn;
+    bool more = ok && walk.next(g);
+    if (more) prefetch(g, 0);
+    for (; ok && more; g = gn) {
+      const int acc = seg & 1, slot = seg & 1;
       const uint32_t parity = (seg >> 1) & 1;
       const uint32_t d = lanes + acc * BN;
+      const int64_t row0 = int64_t(g.m) * 256 + my_rows;
       ++seg;
       if constexpr (kPreMode) {
-        const int h0 = g.n * (BN / 2) + half * (BN / 4);
-        const int64_t row0 = int64_t(g.m) * 256 + rank * 128 + quarter * 32;
-        const int chunks = row0 < a.n ? min(L::kChunks, (a.H - h0 + 31) / 32) : 0;
-        if constexpr (MODE == kPreBwd) {
-          // dh of this tile, while the products run
-          if (a.tma_dh) {
-            fence_proxy_async_smem();  // the staging was read and written by all lanes
-            __syncwarp();
-            if (lane == 0 && chunks > 0) {
-              bulk_wait_read<0>();
-              mbar_arrive_expect_tx(dh_bar, chunks * L::kChunkBytes);
-              for (int c = 0; c < chunks; ++c)
-                tma_load_3d(smem_addr(mine + c * L::kChunkBytes), &map_dh, h0 + c * 32, int(row0),
-                            0, dh_bar);
-            }
-          } else {
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
-            const int rows_here = int(min(int64_t(32), a.n - row0));
-            for (int c = 0; c < chunks; ++c) {
-              const int h = h0 + c * 32 + lane;
-              for (int r = 0; r < 32; ++r)
-                *reinterpret_cast<T*>(mine + c * L::kChunkBytes + value_at<DT>(r, lane)) =
-                    r < rows_here && h < a.H ? static_cast<const T*>(a.dh)[(row0 + r) * a.H + h]
-                                             : rows::from_float<T>(0.f);
-            }
-            __syncwarp();
-          }
-        }
+        // one chunk per warp: units h .. h + 31 of the rows row0 .. row0 + 31
+        const int h = g.n * (BN / 2) + hc;
+        const bool live = live_of(g);
+        bias_w[lane] = next_bias[0];
+        bias_w[32 + lane] = next_bias[1];
+        __syncwarp();
+        more = walk.next(gn);
+        if (more) prefetch(gn, slot ^ 1);
         if (!(ok = waits.wait(tfull0 + 8 * acc, parity))) break;
         tc_fence_after();
-        if constexpr (MODE == kPreBwd) {
-          if (a.tma_dh && chunks > 0) {
-            if (!(ok = waits.wait(dh_bar, dh_phase))) break;
-            dh_phase ^= 1;
-          }
+        if (!live) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+          continue;
         }
+        uint8_t* out = mine;  // kPre: act(g) u; kPreBwd: dh, then dg
+        if constexpr (MODE == kPreBwd && DT != SMC_F32) {
+          out += slot * L::kChunkBytes;
+          if (a.tma_dh) {
+            // a slot's barrier completes a phase for each live tile of it
+            if (!(ok = waits.wait(dh_bar0 + 8 * slot, (dh_phases >> slot) & 1))) break;
+            dh_phases ^= 1u << slot;
+          }
+          if (lane == 0) bulk_wait_read<0>();  // du of the last tile
+        } else {
+          if (lane == 0) bulk_wait_read<0>();  // the last tile's store has left the staging
+        }
+        __syncwarp();
+        uint8_t* out_u = mine + 2 * L::kChunkBytes;  // kPreBwd, 16-bit
+        const int64_t block = (int64_t(g.m) * 2 + rank) * 4 + quarter;
+        float* db = MODE == kPreBwd && a.db_part ? a.db_part + block * 2 * a.H + h : nullptr;
+        const GateRow row{a.bias ? reinterpret_cast<const uint8_t*>(bias_w) : nullptr, out, out_u,
+                          lane, row0 + lane < a.n,
+                          static_cast<const float*>(a.dh) + (row0 + lane) * a.H + h,
+                          a.tma_dh != 0, a.dgu + (row0 + lane) * 6 * a.Hp + h, a.Hp,
+                          a.H - h, db, a.H};
 #pragma unroll
-        for (int c = 0; c < L::kChunks; ++c) {
-          const int h = h0 + c * 32;
-          uint32_t gv[32], uv[32];
-          tmem_ld_x32_async(d + half * (BN / 4) + c * 32, gv);
-          tmem_ld_x32_async(d + BN / 2 + half * (BN / 4) + c * 32, uv);
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t gv[16], uv[16];
+          tmem_ld_x16_async(d + hc + hf * 16, gv);
+          tmem_ld_x16_async(d + BN / 2 + hc + hf * 16, uv);
           tmem_ld_wait();
-          if (c == L::kChunks - 1) {
+          if (hf == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
           }
-          if (c >= chunks) continue;
-          const bool biased = a.bias != nullptr;
-          if (biased) {
-            const T* b = static_cast<const T*>(a.bias);
-            __syncwarp();
-            bias_w[lane] = h + lane < a.H ? rows::to_float(b[h + lane]) : 0.f;
-            bias_w[32 + lane] = h + lane < a.H ? rows::to_float(b[a.H + h + lane]) : 0.f;
-            __syncwarp();
+          gate16<MODE, DT>(gv, uv, hf, a.act, row);
+        }
+        if constexpr (MODE == kPre) {
+          store_chunk<DT>(&map_out, a.tma_out, out, a.out, row0, h, a.n, a.H, lane);
+        } else if constexpr (DT != SMC_F32) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&map_out, smem_addr(out), h, 0, int(row0));
+            tma_store_3d(&map_out, smem_addr(out_u), h, 1, int(row0));
+            bulk_commit();
           }
-          uint8_t* slot = mine + (MODE == kPreBwd ? c : turn) * L::kChunkBytes;
-          uint8_t* slot_u =
-              mine + (L::kChunks + (DT == SMC_F32 ? 0 : c)) * L::kChunkBytes;  // kPreBwd
-          if constexpr (MODE == kPre) {
-            turn ^= 1;
-            if (lane == 0) bulk_wait_read<1>();  // the slot's last store, two stores back
-            __syncwarp();
-          }
-#pragma unroll
-          for (int g8 = 0; g8 < 4; ++g8) {
-            float gg[8], uu[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              gg[i] = __uint_as_float(gv[g8 * 8 + i]);
-              uu[i] = __uint_as_float(uv[g8 * 8 + i]);
+          if (db) {
+            const float sg = column_sum<DT>(out, lane), su = column_sum<DT>(out_u, lane);
+            if (h + lane < a.H) {
+              db[lane] = sg;
+              db[a.H + lane] = su;
             }
-            if (biased) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                gg[i] += bias_w[g8 * 8 + i];
-                uu[i] += bias_w[32 + g8 * 8 + i];
-              }
-            }
-            if constexpr (MODE == kPre) {
-              float v[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = act_value(gg[i], a.act) * uu[i];
-              put8<DT>(slot, lane, g8, v);
-            } else {
-              float dh[8], G[8], U[8];
-              get8<DT>(slot, lane, g8, dh);
-              const bool row_ok = row0 + lane < a.n;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 f = act_both(gg[i], a.act);
-                G[i] = row_ok ? dh[i] * uu[i] * f.y : 0.f;
-                U[i] = row_ok ? dh[i] * f.x : 0.f;
-              }
-              put8<DT>(slot, lane, g8, G);
-              put8<DT>(slot_u, lane, g8, U);
-              if constexpr (DT == SMC_F32) {
-                // three bf16 parts of each, straight to memory
-                if (row_ok && h + g8 * 8 < a.H) {
-                  uint16_t* to = a.dgu + (row0 + lane) * 6 * a.Hp + h + g8 * 8;
-#pragma unroll
-                  for (int s = 0; s < 2; ++s) {
-                    uint32_t w3[3][4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      __nv_bfloat16 lo[3], hi[3];
-                      split3(s ? U[2 * i] : G[2 * i], lo);
-                      split3(s ? U[2 * i + 1] : G[2 * i + 1], hi);
-#pragma unroll
-                      for (int p = 0; p < 3; ++p)
-                        w3[p][i] = uint32_t(__bfloat16_as_ushort(lo[p])) |
-                                   uint32_t(__bfloat16_as_ushort(hi[p])) << 16;
-                    }
-#pragma unroll
-                    for (int p = 0; p < 3; ++p)
-                      *reinterpret_cast<uint4*>(to + (p * 2 + s) * a.Hp) =
-                          make_uint4(w3[p][0], w3[p][1], w3[p][2], w3[p][3]);
-                  }
-                }
-              }
-            }
-          }
-          if constexpr (MODE == kPre) {
-            store_chunk<DT>(&map_out, a.tma_out, slot, a.out, row0, h, a.n, a.H, lane);
-          } else {
-            if constexpr (DT != SMC_F32) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_3d(&map_out, smem_addr(slot), h, 0, int(row0));
-                tma_store_3d(&map_out, smem_addr(slot_u), h, 1, int(row0));
-                bulk_commit();
-              }
-            } else {
-              __syncwarp();
-            }
-            if (a.db_part) {
-              const int64_t block = (int64_t(g.m) * 2 + rank) * 4 + quarter;
-              const float sg = column_sum<DT>(slot, lane), su = column_sum<DT>(slot_u, lane);
-              if (h + lane < a.H) {
-                a.db_part[(block * 2 + 0) * a.H + h + lane] = sg;
-                a.db_part[(block * 2 + 1) * a.H + h + lane] = su;
-              }
-            }
-            __syncwarp();
           }
         }
+        __syncwarp();
       } else {
+        more = walk.next(gn);
         if (!(ok = waits.wait(tfull0 + 8 * acc, parity))) break;
         tc_fence_after();
-        const int c0 = g.n * BN + half * (BN / 2);
-        const int64_t row0 = int64_t(g.m) * 256 + rank * 128 + quarter * 32;
 #pragma unroll 1
         for (int c = 0; c < L::kChunks; ++c) {
-          const int col = c0 + c * 32;
+          const int cc = (group * L::kChunks + c) * 32, col = g.n * BN + cc;
           uint32_t v[32];
-          tmem_ld_x32_async(d + half * (BN / 2) + c * 32, v);
+          tmem_ld_x32_async(d + cc, v);
           tmem_ld_wait();
           if (c == L::kChunks - 1) {
             tc_fence_before();
@@ -623,18 +775,16 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
           if (col >= a.C) continue;
           if constexpr (MODE == kDx) {
             if (row0 >= a.n) continue;
-            uint8_t* slot = mine + turn * L::kChunkBytes;
-            turn ^= 1;
-            if (lane == 0) bulk_wait_read<1>();
+            if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
 #pragma unroll
             for (int g8 = 0; g8 < 4; ++g8) {
               float f[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[g8 * 8 + i]);
-              put8<DT>(slot, lane, g8, f);
+              put8<DT>(mine, lane, g8, f);
             }
-            store_chunk<DT>(&map_out, a.tma_out, slot, a.out, row0, col, a.n, a.C, lane);
+            store_chunk<DT>(&map_out, a.tma_out, mine, a.out, row0, col, a.n, a.C, lane);
           } else {
             const int64_t h = row0 + lane;
             if (g.k0 == 0 && g.k1 == a.k_iters) {
@@ -646,8 +796,8 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
                     to[int64_t(i) * a.H] = rows::from_float<T>(__uint_as_float(v[i]));
               }
             } else {
-              float* to = a.slots + (int64_t(2 * pair + (g.k0 == 0 ? 1 : 0)) * BN + half * (BN / 2) +
-                                     c * 32) * 256 + rank * 128 + quarter * 32 + lane;
+              float* to = a.slots + (int64_t(2 * pair + (g.k0 == 0 ? 1 : 0)) * BN + cc) * 256 +
+                          rank * 128 + quarter * 32 + lane;
 #pragma unroll
               for (int i = 0; i < 32; ++i) to[i * 256] = __uint_as_float(v[i]);
             }
@@ -656,7 +806,13 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
       }
     }
     if (lane == 0) bulk_wait_read<0>();
-    if (MODE == kPreBwd && !ok && lane == 0) mbar_drain(dh_bar, dh_phase);
+    if (MODE == kPreBwd && DT != SMC_F32 && !ok && lane == 0) {  // dh copies may be in flight
+      const uint64_t t0 = global_ns();
+      for (int i = 0; i < 2; ++i)
+        while (!mbar_try_wait(dh_bar0 + 8 * i, (dh_phases >> i) & 1) &&
+               global_ns() - t0 < kAbortDrainNs) {
+        }
+    }
     tc_fence_before();
   }
   __syncthreads();
@@ -669,29 +825,43 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
 }
 
 // dW of the tiles that several pairs worked on: their partial tiles in the
-// order of the pairs.
+// order of the pairs.  A block takes 4 columns (input channels) of a tile, and has
+// up to 8 pairs' values of each in flight.
+constexpr int kJoinCols = 4;
 template <class T>
 __global__ void __launch_bounds__(256)
 k_join_dw(const float* __restrict__ slots, T* __restrict__ dW, int C, int H, int m_tiles,
           int n_tiles, int k_iters, int pairs, int bn) {
   int tile = blockIdx.x;
-  const int64_t all = int64_t(2) * m_tiles * n_tiles * k_iters;
-  const int64_t i0 = int64_t(tile) * k_iters, i1 = i0 + k_iters;
-  const int64_t p0 = ((i0 + 1) * pairs - 1) / all, p1 = (i1 * pairs - 1) / all;
-  if (p0 == p1) return;  // one pair stored it whole
-  const int s = tile / (n_tiles * m_tiles);
-  tile -= s * n_tiles * m_tiles;
-  const int64_t h = int64_t(tile / n_tiles) * 256 + threadIdx.x;
-  if (h >= H) return;
-  const int cl0 = blockIdx.y * 8, c0 = tile % n_tiles * bn + cl0;
-  for (int i = 0; i < 8 && c0 + i < C; ++i) {
-    float v = 0.f;
-    for (int64_t p = p0; p <= p1; ++p) {
-      const int64_t slot = 2 * p + (p * all / pairs > i0 ? 0 : 1);  // as the pair chose it
-      v += slots[(slot * bn + cl0 + i) * 256 + threadIdx.x];
-    }
-    dW[(int64_t(s) * C + c0 + i) * H + h] = rows::from_float<T>(v);
+  __shared__ int64_t range[3];  // first and last pair, the first pair's slot
+  if (threadIdx.x == 0) {
+    const int64_t all = int64_t(2) * m_tiles * n_tiles * k_iters;
+    const int64_t i0 = int64_t(tile) * k_iters, i1 = i0 + k_iters;
+    range[0] = ((i0 + 1) * pairs - 1) / all;
+    range[1] = (i1 * pairs - 1) / all;
+    // its second slot if the tile starts its last segment
+    range[2] = 2 * range[0] + (range[0] * all / pairs > i0 ? 0 : 1);
   }
+  __syncthreads();
+  const int64_t p0 = range[0], p1 = range[1], first = range[2];
+  if (p0 == p1) return;  // one pair stored it whole
+  const int cl0 = blockIdx.y * kJoinCols, c0 = tile / (2 * m_tiles) * bn + cl0;
+  tile %= 2 * m_tiles;
+  const int64_t s = tile / m_tiles, h = int64_t(tile % m_tiles) * 256 + threadIdx.x;
+  if (h >= H) return;
+  const float* from = slots + cl0 * 256 + threadIdx.x;
+  float v[kJoinCols];
+#pragma unroll
+  for (int i = 0; i < kJoinCols; ++i) v[i] = c0 + i < C ? from[first * bn * 256 + i * 256] : 0.f;
+#pragma unroll 8
+  for (int64_t p = p0 + 1; p <= p1; ++p) {
+#pragma unroll
+    for (int i = 0; i < kJoinCols; ++i)
+      if (c0 + i < C) v[i] += from[2 * p * bn * 256 + i * 256];
+  }
+#pragma unroll
+  for (int i = 0; i < kJoinCols; ++i)
+    if (c0 + i < C) dW[(s * C + c0 + i) * H + h] = rows::from_float<T>(v[i]);
 }
 
 // dbias: the sums over 32 rows, added up in a fixed order.
@@ -702,6 +872,7 @@ k_join_db(const float* __restrict__ part, T* __restrict__ dbias, int64_t blocks,
   const int col = blockIdx.x * 32 + threadIdx.x % 32, w = threadIdx.x / 32;
   float s = 0.f;
   if (col < H2)
+#pragma unroll 8
     for (int64_t b = w; b < blocks; b += 32) s += part[b * H2 + col];
   sums[w][threadIdx.x % 32] = s;
   __syncthreads();
@@ -969,7 +1140,7 @@ struct Run {
     if (!map_dgu(&ma, kBK, kBK) || !map_x(&mb, kBK, kBK)) return SMC_ERR_CUDA;
     const int rc = launch_bn<kDw, DT>(bn, ma, mb, mo, md, a, s);
     if (rc != SMC_OK) return rc;
-    k_join_dw<T><<<dim3(tiles, bn / 8), 256, 0, s>>>(a.slots, static_cast<T*>(dW), g.cin, g.hidden,
+    k_join_dw<T><<<dim3(tiles, bn / kJoinCols), 256, 0, s>>>(a.slots, static_cast<T*>(dW), g.cin, g.hidden,
                                                      a.m_tiles, a.n_tiles, a.k_iters, a.pairs, bn);
     return cudaGetLastError() == cudaSuccess ? SMC_OK : SMC_ERR_CUDA;
   }
