@@ -138,39 +138,40 @@ def _dev_ptr(t: torch.Tensor, name: str, dtype=None) -> int:
 
 
 class _Call:
-    """The device and stream of one row-operator call: `with _Call(x, stream) as c`
-    makes x's device current; c.empty() allocates results and workspaces on the
-    call's stream, and with an explicit stream c.keep() tells the allocator that
-    the call reads a tensor there, so that its memory is not reused too early."""
+    """The device and stream of one row-operator call.  Inside `with _Call(x,
+    stream) as c`, x's device is current and tensors are allocated on the call's
+    stream (c.stream: its raw pointer).  With an explicit stream, c.keep() tells
+    the allocator that the call uses a tensor there, so that its memory is not
+    given away too early."""
+
+    __slots__ = ("given", "stream", "_device", "_contexts")
 
     def __init__(self, x: torch.Tensor, stream: Optional[torch.cuda.Stream]):
-        self.device, self.stream = x.device, stream
+        self.given, self._device = stream, x.device
         if stream is not None and stream.device != x.device:
             raise ValueError("stream must be on the tensors' device")
-        self.contexts = [torch.cuda.device(x.device)]
-        if stream is not None:
-            self.contexts.append(torch.cuda.stream(stream))
 
     def __enter__(self):
-        for c in self.contexts:
+        index = self._device.index
+        self._contexts = ()
+        if self.given is not None:
+            self._contexts = (torch.cuda.device(index), torch.cuda.stream(self.given))
+        elif torch.cuda.current_device() != index:
+            self._contexts = (torch.cuda.device(index),)
+        for c in self._contexts:
             c.__enter__()
+        self.stream = torch.cuda.current_stream(index).cuda_stream
         return self
 
     def __exit__(self, *exc):
-        for c in reversed(self.contexts):
+        for c in reversed(self._contexts):
             c.__exit__(*exc)
 
-    def empty(self, shape, dtype) -> torch.Tensor:
-        return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def pointer(self) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream
-
     def keep(self, *tensors) -> None:
-        if self.stream is not None:
+        if self.given is not None:
             for t in tensors:
                 if t is not None:
-                    t.record_stream(self.stream)
+                    t.record_stream(self.given)
 
 
 def _operand(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape,
@@ -180,7 +181,7 @@ def _operand(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape,
     if t is None:
         return None
     ptr = _dev_ptr(t, name, like.dtype if dtype is None else dtype)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.device != like.device:
         raise ValueError(f"{name} must be on {like.device}, got {t.device}")
@@ -398,9 +399,9 @@ def smc_layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
     bp = _operand(beta, "beta", x, (c,), torch.float32)
     with _Call(x, stream) as call:
         if out is None:
-            out = call.empty((n, c), x.dtype)
+            out = torch.empty_like(x)
         op = _operand(out, "out", x, (n, c))
-        _check(lib().smc_layer_norm(xp, gp, bp, op, n, c, code, float(eps), call.pointer()),
+        _check(lib().smc_layer_norm(xp, gp, bp, op, n, c, code, float(eps), call.stream),
                "smc_layer_norm")
         call.keep(x, gamma, beta, out)
     return out
@@ -426,17 +427,17 @@ def smc_layer_norm_backward(x: torch.Tensor, gamma: Optional[torch.Tensor],
     yp = _operand(grad_out, "grad_out", x, (n, c))
     with _Call(x, stream) as call:
         if grad_in is None:
-            grad_in = call.empty((n, c), x.dtype)
+            grad_in = torch.empty_like(x)
         ip = _operand(grad_in, "grad_in", x, (n, c))
         dgamma = dbeta = None
         if gamma is not None:
-            dgamma, dbeta = call.empty((c,), torch.float32), call.empty((c,), torch.float32)
+            dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
         size = smc_layer_norm_backward_workspace(n, c, x.dtype)
-        work = call.empty((size,), torch.uint8)
+        work = torch.empty(size, dtype=torch.uint8, device=x.device)
         _check(lib().smc_layer_norm_backward(
             xp, gp, yp, ip, None if dgamma is None else dgamma.data_ptr(),
             None if dbeta is None else dbeta.data_ptr(), n, c, code, float(eps), work.data_ptr(),
-            size, call.pointer()), "smc_layer_norm_backward")
+            size, call.stream), "smc_layer_norm_backward")
         call.keep(x, gamma, grad_out, grad_in)
     return grad_in, dgamma, dbeta
 
@@ -462,18 +463,22 @@ def smc_gated_forward(handle: int, feats: torch.Tensor, W: torch.Tensor, out: to
                       activation: str = "silu",
                       stream: Optional[torch.cuda.Stream] = None) -> None:
     """out = act(feats @ W[0] + bias[0]) * (feats @ W[1] + bias[1])."""
+    _gated_forward(handle, _handle_rows(handle, feats), feats, W, out, cin, hidden, bias,
+                   activation, stream)
+
+
+def _gated_forward(handle, n, feats, W, out, cin, hidden, bias, activation, stream=None) -> None:
     code = _rows(feats, "feats")
-    n = _handle_rows(handle, feats)
     fp = _operand(feats, "feats", feats, (n, cin))
     wp = _operand(W, "W", feats, (2, cin, hidden))
     bp = _operand(bias, "bias", feats, (2, hidden))
     op = _operand(out, "out", feats, (n, hidden))
     with _Call(feats, stream) as call:
         size = smc_gated_workspace(handle, cin, hidden, feats.dtype, False)
-        work = call.empty((size,), torch.uint8) if size else None
+        work = torch.empty(size, dtype=torch.uint8, device=feats.device) if size else None
         _check(lib().smc_gated_forward(handle, fp, wp, bp, op, int(cin), int(hidden), code,
                                        ACT_CODE[activation], work.data_ptr() if size else None,
-                                       size, call.pointer()), "smc_gated_forward")
+                                       size, call.stream), "smc_gated_forward")
         call.keep(feats, W, bias, out)
 
 
@@ -484,8 +489,13 @@ def smc_gated_backward(handle: int, feats: torch.Tensor, W: torch.Tensor, grad_o
                        stream: Optional[torch.cuda.Stream] = None) -> None:
     """Gradients of smc_gated_forward into those of grad_in, grad_W and
     grad_bias that are not None."""
+    _gated_backward(handle, _handle_rows(handle, feats), feats, W, grad_out, grad_in, grad_W,
+                    grad_bias, cin, hidden, bias, activation, stream)
+
+
+def _gated_backward(handle, n, feats, W, grad_out, grad_in, grad_W, grad_bias, cin, hidden, bias,
+                    activation, stream=None) -> None:
     code = _rows(feats, "feats")
-    n = _handle_rows(handle, feats)
     fp = _operand(feats, "feats", feats, (n, cin))
     wp = _operand(W, "W", feats, (2, cin, hidden))
     bp = _operand(bias, "bias", feats, (2, hidden))
@@ -495,10 +505,10 @@ def smc_gated_backward(handle: int, feats: torch.Tensor, W: torch.Tensor, grad_o
     dbp = _operand(grad_bias, "grad_bias", feats, (2, hidden))
     with _Call(feats, stream) as call:
         size = smc_gated_workspace(handle, cin, hidden, feats.dtype, True)
-        work = call.empty((size,), torch.uint8) if size else None
+        work = torch.empty(size, dtype=torch.uint8, device=feats.device) if size else None
         _check(lib().smc_gated_backward(handle, fp, wp, bp, yp, ip, dwp, dbp, int(cin),
                                         int(hidden), code, ACT_CODE[activation],
-                                        work.data_ptr() if size else None, size, call.pointer()),
+                                        work.data_ptr() if size else None, size, call.stream),
                "smc_gated_backward")
         call.keep(feats, W, bias, grad_out, grad_in, grad_W, grad_bias)
 
@@ -520,10 +530,10 @@ def smc_dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
     sp = _operand(state, "state", x, (2,), torch.int64)
     with _Call(x, stream) as call:
         if out is None:
-            out = call.empty(x.shape, x.dtype)
+            out = torch.empty_like(x)
         op = _operand(out, "out", x, x.shape)
         _check(lib().smc_dropout(xp, rp, op, x.numel(), DTYPE_CODE[x.dtype], float(p), seed, offset,
-                                 sp, call.pointer()), "smc_dropout")
+                                 sp, call.stream), "smc_dropout")
         call.keep(x, residual, state, out)
     return out
 
@@ -692,7 +702,7 @@ class SubMIndex:
         cin, hidden = self._gated_shape(feats, W)
         if out is None:
             out = torch.empty((self.n, hidden), dtype=feats.dtype, device=feats.device)
-        smc_gated_forward(self.handle, feats, W, out, cin, hidden, bias, activation)
+        _gated_forward(self.handle, self.n, feats, W, out, cin, hidden, bias, activation)
         return out
 
     def gated_backward(self, feats: torch.Tensor, W: torch.Tensor, grad_out: torch.Tensor,
@@ -702,8 +712,8 @@ class SubMIndex:
         cin, hidden = self._gated_shape(feats, W)
         grad_in, grad_W = torch.empty_like(feats), torch.empty_like(W)
         grad_bias = None if bias is None else torch.empty_like(bias)
-        smc_gated_backward(self.handle, feats, W, grad_out, grad_in, grad_W, grad_bias, cin,
-                           hidden, bias, activation)
+        _gated_backward(self.handle, self.n, feats, W, grad_out, grad_in, grad_W, grad_bias, cin,
+                        hidden, bias, activation)
         return grad_in, grad_W, grad_bias
 
     def _gated_shape(self, feats: torch.Tensor, W: torch.Tensor) -> tuple:

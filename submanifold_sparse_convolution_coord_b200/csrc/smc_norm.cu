@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "smc_internal.h"
+#include "smc_ptx.cuh"
 #include "smc_rows.cuh"
 
 namespace smc {
@@ -112,56 +113,314 @@ __device__ __forceinline__ float2 share_stats(const RowShare<T, V, G, VECS>& x, 
   return make_float2(mean, rsqrtf(group_sum<G>(s, smem) * inv_c + eps));
 }
 
-// Rows per group and step: enough bytes in flight per thread for short rows
-// (two vectors at least), one for long ones.
-template <int VECS>
-constexpr int rows_per_step() {
-  return VECS == 1 ? 4 : (VECS == 2 ? 2 : 1);
+// V consecutive floats (16-byte aligned when V is a multiple of 4).
+template <int V>
+__device__ __forceinline__ void load_floats(const float* p, float (&v)[V]) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + j);
+      v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = p[j];
+  }
+}
+
+// Rows per group: enough bytes in flight per thread for short rows.
+template <class T, int V, int VECS>
+constexpr int rows_per_group() {
+  constexpr int bytes = VECS * V * int(sizeof(T));
+  return bytes <= 16 ? 4 : (bytes <= 32 ? 2 : 1);
+}
+
+// Small blocks for rows of up to a warp: more of them are at different stages
+// on an SM (4,749,279 x 64 bf16: 238 us with 256 threads, TODO us with 128).
+template <int G>
+constexpr int norm_threads() {
+  return G <= 32 ? 128 : kThreads;
 }
 
 template <class T, int V, int G, int VECS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(norm_threads<G>(), G > 32 ? 1 : (VECS == 1 ? 8 : (VECS * V <= 16 ? 4 : 2)))
 k_norm(const T* x, const float* __restrict__ gamma, const float* __restrict__ beta, T* out,
        int64_t n, int c, float inv_c, float eps) {
-  constexpr int R = rows_per_step<VECS>();
-  constexpr int kGroups = kThreads / G;
+  constexpr int R = rows_per_group<T, V, VECS>();
+  constexpr int kGroups = norm_threads<G>() / G;
   __shared__ float smem[kThreads / 32];
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
-  const int64_t r0 = blockIdx.x * int64_t(kGroups * R) + group;
+  const int64_t base = blockIdx.x * int64_t(kGroups * R);
+  const int rows_here = int(min(n - base, int64_t(kGroups * R)));
+  x += base * c;
+  out += base * c;
   RowShare<T, V, G, VECS> share[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    const int64_t r = r0 + k * kGroups;
-    share[k].load(x + r * c, lane, c, r < n);
+    const int r = group + k * kGroups;
+    share[k].load(x + int64_t(r) * c, lane, c, r < rows_here);
   }
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    const int64_t r = r0 + k * kGroups;
-    const float2 st = share_stats(share[k], lane, c, inv_c, eps, smem);
-    if (r >= n) continue;
+  // one vector a thread: gamma and beta in registers for all R rows
+  constexpr bool kHold = VECS == 1;
+  float gm[kHold ? VECS : 1][V], bt[kHold ? VECS : 1][V];
+  if constexpr (kHold) {
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
       const int at = (lane + i * G) * V;
+      if (gamma && at < c) load_floats(gamma + at, gm[i]);
+      if (beta && at < c) load_floats(beta + at, bt[i]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int r = group + k * kGroups;
+    const float2 st = share_stats(share[k], lane, c, inv_c, eps, smem);
+    if (r >= rows_here) continue;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int at = (lane + i * G) * V, h = kHold ? i : 0;
       if (at >= c) continue;
+      if constexpr (!kHold) {
+        if (gamma) load_floats(gamma + at, gm[0]);
+        if (beta) load_floats(beta + at, bt[0]);
+      }
       Vec<T, V> o;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         float v = (share[k].value(i, j) - st.x) * st.y;
-        if (gamma) v *= gamma[at + j];
-        if (beta) v += beta[at + j];
+        if (gamma) v *= gm[h][j];
+        if (beta) v += bt[h][j];
         o.v[j] = rows::from_float<T>(v);
       }
-      *reinterpret_cast<Vec<T, V>*>(out + r * c + at) = o;
+      *reinterpret_cast<Vec<T, V>*>(out + int64_t(r) * c + at) = o;
     }
   }
 }
 
-// Blocks walk the rows with a stride; a thread keeps the sums of dgamma and
-// dbeta for its columns, which are the same in every row, and the block joins
-// its groups' sums at the end: part[block][2][c].
+// ---------------------------------------------------------------------------
+// backward, rows of up to a warp
+// ---------------------------------------------------------------------------
+// Pairs of floats: one instruction for two of them (add, multiply, multiply-add
+// on 64-bit register pairs), which matters because the backward does about 14
+// operations per element next to its 6 bytes.
+__device__ __forceinline__ uint64_t bits2(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
+__device__ __forceinline__ float2 float2_of(uint64_t v) { return *reinterpret_cast<float2*>(&v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return float2_of(r);
+}
+
+// A lane's share of a row as pairs: value k is vector k / V, element k % V.
+template <class T, int V, int G, int VECS, bool WHOLE>
+struct Share {
+  static constexpr int N = VECS * V, P = (N + 1) / 2;
+  // column of value k
+  static __device__ __forceinline__ int column(int lane, int k) {
+    return (lane + k / V * G) * V + k % V;
+  }
+  // From a row in shared memory; zeros outside it (WHOLE: there is no outside).
+  static __device__ __forceinline__ void load(const T* row, int lane, int c, float2 (&v)[P]) {
+    float f[2 * P];
+    f[2 * P - 1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int at = (lane + i * G) * V;
+      Vec<T, V> q;
+      if constexpr (WHOLE) {
+        q = *reinterpret_cast<const Vec<T, V>*>(row + at);
+      } else {
+        q = Vec<T, V>{};
+        if (at < c) q = *reinterpret_cast<const Vec<T, V>*>(row + at);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[i * V + j] = rows::to_float(q.v[j]);
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) v[p] = make_float2(f[2 * p], f[2 * p + 1]);
+  }
+};
+
+constexpr int kRingWarps = 8;
+// Two blocks per SM with three slots a warp, or, where a lane's share of a row
+// is more than 16 values (registers for one block), one with four.
+constexpr int ring_blocks(int values) { return values > 16 ? 1 : 2; }
+constexpr int ring_stages(int values) { return values > 16 ? 4 : 3; }
+
+// Each warp streams its own chunks of `chunk_rows` consecutive rows of x and dy
+// through a ring of slots in shared memory, filled by 16-byte
+// asynchronous copies from the 16-byte boundary below the chunk: what is in
+// flight does not depend on registers, and rows of any length arrive with whole
+// 16-byte accesses.  A lane keeps the sums of dgamma and dbeta for
+// its columns, which are the same in every row; the block joins them at the
+// end: part[block][2][c].  (209,715 x 128 fp16: 37 us with loads to registers,
+// TODO us so.)
+template <class T, int V, int G, int VECS, bool WHOLE>
+__global__ void __launch_bounds__(32 * kRingWarps, ring_blocks(VECS * V))
+k_norm_bwd(const T* __restrict__ x, const float* __restrict__ gamma, const T* __restrict__ dy,
+           T* __restrict__ dx, float* __restrict__ part, int64_t n, int c, int chunk_rows,
+           int slot_bytes, float inv_c, float eps) {
+  using S = Share<T, V, G, VECS, WHOLE>;
+  constexpr int P = S::P, N = S::N, kRingStages = ring_stages(N);
+  constexpr bool kKeep = N <= 20;  // dy * gamma stays in registers, else dy is read again
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x / 32, wl = threadIdx.x % 32, lane = wl % G, group = wl / G;
+  const int chunk_bytes = chunk_rows * c * int(sizeof(T));
+  uint8_t* ring = smem + warp * (kRingStages * 2) * slot_bytes;  // slot: x, then dy
+  const int64_t total = n * c * int64_t(sizeof(T));
+  const int64_t chunks = (n + chunk_rows - 1) / chunk_rows;
+  const int64_t stride = int64_t(gridDim.x) * kRingWarps;
+
+  float2 gm[P], dg[P] = {}, db[P] = {};
+#pragma unroll
+  for (int k = 0; k < 2 * P; ++k) {
+    const int col = S::column(lane, k);
+    const float v = gamma && k < N && col < c ? gamma[col] : 1.f;
+    (k & 1 ? gm[k / 2].y : gm[k / 2].x) = v;
+  }
+  const uint32_t ring0 = ptx::smem_addr(ring) + wl * 16;
+  auto fill = [&](int64_t chunk, int slot) {
+    if (chunk < chunks) {
+      const int64_t from = chunk * chunk_bytes & ~int64_t(15);
+      const uint32_t to = ring0 + slot * 2 * slot_bytes;
+      const uint8_t* px = reinterpret_cast<const uint8_t*>(x) + from + wl * 16;
+      const uint8_t* pd = reinterpret_cast<const uint8_t*>(dy) + from + wl * 16;
+      if (from + slot_bytes <= total) {
+        for (int at = 0; at < slot_bytes - wl * 16; at += 512) {
+          ptx::cp_async_16(to + at, px + at, 16);
+          ptx::cp_async_16(to + slot_bytes + at, pd + at, 16);
+        }
+      } else {  // nothing behind the last row is read
+        for (int at = 0; at < slot_bytes - wl * 16; at += 512) {
+          const int64_t left = total - from - wl * 16 - at;
+          const uint32_t bytes = left >= 16 ? 16u : (left > 0 ? uint32_t(left) : 0u);
+          ptx::cp_async_16(to + at, left > 0 ? px + at : reinterpret_cast<const uint8_t*>(x), bytes);
+          ptx::cp_async_16(to + slot_bytes + at,
+                           left > 0 ? pd + at : reinterpret_cast<const uint8_t*>(dy), bytes);
+        }
+      }
+    }
+    ptx::cp_async_commit();
+  };
+  int64_t chunk = blockIdx.x * int64_t(kRingWarps) + warp;
+#pragma unroll
+  for (int k = 0; k < kRingStages - 1; ++k) fill(chunk + k * stride, k);
+  for (int slot = 0; chunk < chunks; chunk += stride) {
+    ptx::cp_async_wait_group<kRingStages - 2>();
+    __syncwarp();  // every lane's copies have landed; the slot before this one is free
+    fill(chunk + (kRingStages - 1) * stride, slot == 0 ? kRingStages - 1 : slot - 1);
+    const uint8_t* here = ring + slot * 2 * slot_bytes + (chunk * chunk_bytes & 15);
+    const T* xs = reinterpret_cast<const T*>(here);
+    const T* ds = reinterpret_cast<const T*>(here + slot_bytes);
+    slot = slot + 1 == kRingStages ? 0 : slot + 1;
+    for (int row = group; row < chunk_rows; row += 32 / G) {
+      const int64_t r = chunk * chunk_rows + row;
+      const bool ok = r < n;
+      float2 xc[P], g[P];
+      S::load(xs + row * c, lane, c, xc);
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int p = 0; p < P; ++p) s = add2(s, xc[p]);
+      const float mean = group_sum<G>(s.x + s.y, nullptr) * inv_c;
+      s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float2 m = make_float2(-mean, -mean);
+        if constexpr (!WHOLE || N % 2 != 0) {  // columns outside the row stay 0
+          if (2 * p + 1 >= N || S::column(lane, 2 * p + 1) >= c) m.y = 0.f;
+          if (S::column(lane, 2 * p) >= c) m.x = 0.f;
+        }
+        xc[p] = add2(xc[p], m);
+        s = fma2(xc[p], xc[p], s);
+      }
+      float rstd = rsqrtf(group_sum<G>(s.x + s.y, nullptr) * inv_c + eps);
+      if (!ok) rstd = 0.f;  // a row that does not exist: eps = 0 made it infinite
+      const float2 rr = make_float2(rstd, rstd);
+      float2 s1 = make_float2(0.f, 0.f), s2 = s1;
+      S::load(ds + row * c, lane, c, g);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const float2 d = g[p];
+        db[p] = add2(db[p], d);
+        dg[p] = fma2(mul2(d, rr), xc[p], dg[p]);
+        const float2 q = mul2(d, gm[p]);
+        s1 = add2(s1, q);
+        s2 = fma2(q, xc[p], s2);
+        if (kKeep) g[p] = q;
+      }
+      const float2 sums = group_sum2<G>(make_float2(s1.x + s1.y, s2.x + s2.y), nullptr);
+      // dx = r g - r mean(g) - xc r^3 mean(g xc)
+      const float k1 = -sums.x * inv_c * rstd, k2 = -sums.y * inv_c * rstd * rstd * rstd;
+      const float2 kk1 = make_float2(k1, k1), kk2 = make_float2(k2, k2);
+      if constexpr (!kKeep) {
+        S::load(ds + row * c, lane, c, g);
+#pragma unroll
+        for (int p = 0; p < P; ++p) g[p] = mul2(g[p], gm[p]);
+      }
+      float out[2 * P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const float2 o = fma2(xc[p], kk2, fma2(g[p], rr, kk1));
+        out[2 * p] = o.x;
+        out[2 * p + 1] = o.y;
+      }
+      if (!ok) continue;
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+        const int at = (lane + i * G) * V;
+        if (!WHOLE && at >= c) continue;
+        Vec<T, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o.v[j] = rows::from_float<T>(out[i * V + j]);
+        *reinterpret_cast<Vec<T, V>*>(dx + r * c + at) = o;
+      }
+    }
+  }
+  ptx::cp_async_wait_group<0>();
+  if (!part) return;
+  // join the warp's groups by shuffles, the warps through shared memory
+  __syncthreads();  // the rings are free
+  float* acc = reinterpret_cast<float*>(smem);  // [kRingWarps][2][c]
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    float a = k & 1 ? dg[k / 2].y : dg[k / 2].x, b = k & 1 ? db[k / 2].y : db[k / 2].x;
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    const int col = S::column(lane, k);
+    if (group == 0 && col < c) {
+      acc[(warp * 2 + 0) * c + col] = a;
+      acc[(warp * 2 + 1) * c + col] = b;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * c; i += 32 * kRingWarps) {
+    float t = 0.f;
+    for (int w = 0; w < kRingWarps; ++w) t += acc[w * 2 * c + i];
+    part[blockIdx.x * 2 * int64_t(c) + i] = t;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// backward, rows of more than a warp
+// ---------------------------------------------------------------------------
+// As k_norm_bwd, but a row takes G = 64 to 256 threads, each with enough
+// vectors of it that loads to registers, one row ahead, keep memory busy.
 template <class T, int V, int G, int VECS>
 __global__ void __launch_bounds__(kThreads)
-k_norm_bwd(const T* __restrict__ x, const float* __restrict__ gamma, const T* __restrict__ dy,
+k_norm_bwd_wide(const T* __restrict__ x, const float* __restrict__ gamma, const T* __restrict__ dy,
            T* __restrict__ dx, float* __restrict__ part, int64_t n, int c, float inv_c, float eps) {
   constexpr int kGroups = kThreads / G;
   __shared__ float smem[kThreads / 32];
@@ -177,12 +436,17 @@ k_norm_bwd(const T* __restrict__ x, const float* __restrict__ gamma, const T* __
       gm[i][j] = gamma && at < c ? gamma[at] : 1.f;
     }
   // the block's rows run out together, so that every thread takes part in the sums
-  for (int64_t base = blockIdx.x * int64_t(kGroups); base < n; base += int64_t(gridDim.x) * kGroups) {
+  const int64_t step = int64_t(gridDim.x) * kGroups;
+  int64_t base = blockIdx.x * int64_t(kGroups);
+  RowShare<T, V, G, VECS> xn, gn;  // the next row, asked for while this one is worked on
+  xn.load(x + (base + group) * c, lane, c, base + group < n);
+  gn.load(dy + (base + group) * c, lane, c, base + group < n);
+  for (; base < n; base += step) {
     const int64_t r = base + group;
     const bool ok = r < n;
-    RowShare<T, V, G, VECS> xs, gs;
-    xs.load(x + r * c, lane, c, ok);
-    gs.load(dy + r * c, lane, c, ok);
+    const RowShare<T, V, G, VECS> xs = xn, gs = gn;
+    xn.load(x + (r + step) * c, lane, c, r + step < n);
+    gn.load(dy + (r + step) * c, lane, c, r + step < n);
     float2 st = share_stats(xs, lane, c, inv_c, eps, smem);
     if (!ok) st.y = 0.f;  // eps = 0 made it infinite
     float2 s = make_float2(0.f, 0.f);
@@ -362,42 +626,89 @@ int sm_count() {
   return sms;
 }
 
-// How a row of c values is dealt to a group: the widest vector that divides
-// the row, then the narrowest group whose threads hold at most kVecs vectors.
-constexpr int kVecs = 4;
+// How a row of c values is dealt to a group.  The widest vector that divides
+// the row; vectors of 8 bytes and more: the narrowest group whose threads hold
+// one vector (up to a warp) or up to four; narrower ones, which carry few
+// bytes each: a warp with up to 20 a thread, so that the row's sums stay
+// shuffles (26,213 rows of 515 fp32 values, backward: 47.6 us with 128 threads
+// and block barriers, TODO us with a warp), then 256 threads.
 struct Deal {
   int v, g, vecs;  // vecs = 0: the row is too long for registers
 };
-Deal deal(int64_t c, int elem) {
+template <class I>
+Deal deal(I c, int elem) {
   Deal d{16 / elem, 1, 0};
   while (c % d.v != 0) d.v /= 2;
   const int64_t vectors = c / d.v;
-  // narrow vectors carry few bytes: more of them per thread
-  const int most = d.v * elem >= 8 ? kVecs : 2 * kVecs;
-  while (d.g < kThreads && vectors > int64_t(d.g) * (d.g < 32 ? 1 : most)) d.g *= 2;
+  const bool narrow = d.v * elem < 8;
+  if (!narrow) {
+    while (d.g < kThreads && vectors > int64_t(d.g) * (d.g < 32 ? 1 : 4)) d.g *= 2;
+    const int64_t need = (vectors + d.g - 1) / d.g;
+    if (need <= 4) d.vecs = int(need);
+    return d;
+  }
+  while (d.g < 32 && vectors > d.g) d.g *= 2;
+  if (vectors > 32 * 20) d.g = kThreads;
   const int64_t need = (vectors + d.g - 1) / d.g;
-  d.vecs = need <= most ? (need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : 8) : 0;
+  for (int k : {1, 2, 4, 8, 12, 16, 20})
+    if (d.vecs == 0 && need <= k && (d.g <= 32 || k <= 8)) d.vecs = k;
   return d;
 }
 
-template <class T, class F>
+// The backward's ring kernel has the rows in shared memory, where a warp may
+// read them in any way: from eight vectors on, two vectors a thread, which
+// halves the steps of the sums.
+template <class I>
+Deal deal_bwd(I c, int elem) {
+  Deal d = deal(c, elem);
+  const int64_t vectors = c / d.v;
+  if (d.v * elem >= 8 && d.g >= 16 && d.g <= 32 && vectors <= 64) {
+    d.g = vectors <= 16 ? 8 : (vectors <= 32 ? 16 : 32);
+    d.vecs = 2;
+  }
+  return d;
+}
+
+// f(V, G, VECS) as compile-time values.
+template <class T, bool BWD, class F>
 int by_deal(const Deal& d, F&& f) {
-  auto with = [&](auto v, auto g) {
+#define SMC_VECS(K) \
+  case K:           \
+    return f(v, g, std::integral_constant<int, K>())
+  auto with = [&](auto v, auto g) -> int {
     constexpr int V = decltype(v)::value, G = decltype(g)::value;
-    if constexpr (G < 32) {  // one vector a thread, by the rule above
-      return f(v, g, std::integral_constant<int, 1>());
-    } else {
+    constexpr bool narrow = V * sizeof(T) < 8;
+    if constexpr (G < 32) {
+      if constexpr (BWD && !narrow && G >= 8)
+        if (d.vecs == 2) return f(v, g, std::integral_constant<int, 2>());
+      if (d.vecs == 1) return f(v, g, std::integral_constant<int, 1>());
+    } else if constexpr (!narrow) {
       switch (d.vecs) {
-        case 1: return f(v, g, std::integral_constant<int, 1>());
-        case 2: return f(v, g, std::integral_constant<int, 2>());
-        case 4: return f(v, g, std::integral_constant<int, 4>());
-        default:
-          if constexpr (V * sizeof(T) < 8) return f(v, g, std::integral_constant<int, 8>());
-          return int(SMC_ERR_INVALID);
+        SMC_VECS(1);
+        SMC_VECS(2);
+        SMC_VECS(3);
+        SMC_VECS(4);
+      }
+    } else if constexpr (G == 32) {
+      switch (d.vecs) {
+        SMC_VECS(1);
+        SMC_VECS(2);
+        SMC_VECS(4);
+        SMC_VECS(8);
+        SMC_VECS(12);
+        SMC_VECS(16);
+        SMC_VECS(20);
+      }
+    } else if constexpr (G == kThreads) {
+      switch (d.vecs) {
+        SMC_VECS(4);
+        SMC_VECS(8);
       }
     }
+    return int(SMC_ERR_INVALID);
   };
-  auto wide = [&](auto v) {
+#undef SMC_VECS
+  auto wide = [&](auto v) -> int {
     switch (d.g) {
       case 1: return with(v, std::integral_constant<int, 1>());
       case 2: return with(v, std::integral_constant<int, 2>());
@@ -420,12 +731,31 @@ int by_deal(const Deal& d, F&& f) {
   }
 }
 
-// Blocks of the backward kernel: a few per SM (each leaves one partial sum),
-// and no more than there are groups of rows.
-int64_t bwd_blocks(int64_t n, const Deal& d) {
-  const int64_t groups = kThreads / d.g;
-  return std::max<int64_t>(1, std::min<int64_t>((n + groups - 1) / groups, int64_t(sm_count()) * 4));
-}
+// Launch of the backward kernels.  Ring (groups of up to a warp): chunks of
+// up to 2 KB, whole passes of a warp; one or two blocks per SM.  Wide groups: a few blocks per SM.  Each block leaves one partial
+// sum, and there are no more blocks than work.
+struct BwdPlan {
+  Deal d;
+  int chunk_rows = 0, slot_bytes = 0, smem = 0;
+  int64_t blocks = 1;
+  BwdPlan(int64_t n, int64_t c, int elem) : d(deal_bwd(c, elem)) {
+    if (d.vecs == 0) return;
+    const int64_t most = int64_t(sm_count());
+    if (d.g > 32) {
+      const int64_t groups = kThreads / d.g;
+      blocks = std::max<int64_t>(1, std::min((n + groups - 1) / groups, most * 4));
+      return;
+    }
+    const int pass = 32 / d.g;
+    chunk_rows = pass * int(std::max<int64_t>(1, 2048 / (pass * c * elem)));
+    slot_bytes = int((chunk_rows * c * elem + 15 + 15) / 16 * 16);
+    const int values = d.vecs * d.v;
+    smem = std::max(kRingWarps * ring_stages(values) * 2 * slot_bytes, kRingWarps * 2 * int(c) * 4);
+    const int64_t chunks = (n + chunk_rows - 1) / chunk_rows;
+    blocks = std::max<int64_t>(1, std::min((chunks + kRingWarps - 1) / kRingWarps,
+                                           most * ring_blocks(values)));
+  }
+};
 
 }  // namespace
 
@@ -440,10 +770,10 @@ int layer_norm(const void* x, const float* gamma, const float* beta, void* out, 
       k_norm_long<T><<<unsigned(n), kThreads, 0, s>>>(in, gamma, beta, o, c, eps);
       return launched();
     }
-    return by_deal<T>(d, [&](auto v, auto g, auto vecs) {
+    return by_deal<T, false>(d, [&](auto v, auto g, auto vecs) {
       constexpr int V = decltype(v)::value, G = decltype(g)::value, K = decltype(vecs)::value;
-      const int64_t step = kThreads / G * rows_per_step<K>();
-      k_norm<T, V, G, K><<<unsigned((n + step - 1) / step), kThreads, 0, s>>>(
+      const int64_t step = norm_threads<G>() / G * rows_per_group<T, V, K>();
+      k_norm<T, V, G, K><<<unsigned((n + step - 1) / step), norm_threads<G>(), 0, s>>>(
           in, gamma, beta, o, n, int(c), 1.f / float(c), eps);
       return launched();
     });
@@ -451,11 +781,11 @@ int layer_norm(const void* x, const float* gamma, const float* beta, void* out, 
 }
 
 int64_t layer_norm_backward_workspace(int64_t n, int64_t c, int dtype) {
-  const Deal d = deal(c, dtype == SMC_F32 ? 4 : 2);
   if (n == 0) return 0;
-  if (d.vecs == 0)
+  const BwdPlan p(n, c, dtype == SMC_F32 ? 4 : 2);
+  if (p.d.vecs == 0)
     return n * int64_t(sizeof(float2)) + chunks(n) * 2 * c * int64_t(sizeof(float));
-  return bwd_blocks(n, d) * 2 * c * int64_t(sizeof(float));
+  return p.blocks * 2 * c * int64_t(sizeof(float));
 }
 
 int layer_norm_backward(const void* x, const float* gamma, const void* dy, void* dx,
@@ -465,10 +795,10 @@ int layer_norm_backward(const void* x, const float* gamma, const void* dy, void*
     using T = decltype(tag);
     const T *in = static_cast<const T*>(x), *g_out = static_cast<const T*>(dy);
     T* g_in = static_cast<T*>(dx);
-    const Deal d = deal(c, sizeof(T));
+    const BwdPlan p(n, c, sizeof(T));
     float* part = static_cast<float*>(workspace);
     int64_t parts = 0;
-    if (n > 0 && d.vecs == 0) {
+    if (n > 0 && p.d.vecs == 0) {
       float2* stats = static_cast<float2*>(workspace);
       part = reinterpret_cast<float*>(stats + n);
       k_norm_bwd_long<T><<<unsigned(n), kThreads, 0, s>>>(in, gamma, g_out, g_in, stats, c, eps);
@@ -478,13 +808,37 @@ int layer_norm_backward(const void* x, const float* gamma, const void* dy, void*
                          0, s>>>(in, g_out, stats, part, n, c);
       }
     } else if (n > 0) {
-      const int64_t blocks = bwd_blocks(n, d);
-      if (dgamma) parts = blocks;
-      const int rc = by_deal<T>(d, [&](auto v, auto g, auto vecs) {
+      if (dgamma) parts = p.blocks;
+      float* to = dgamma ? part : nullptr;
+      const int rc = by_deal<T, true>(p.d, [&](auto v, auto g, auto vecs) {
         constexpr int V = decltype(v)::value, G = decltype(g)::value, K = decltype(vecs)::value;
-        k_norm_bwd<T, V, G, K><<<unsigned(blocks), kThreads, 0, s>>>(
-            in, gamma, g_out, g_in, dgamma ? part : nullptr, n, int(c), 1.f / float(c), eps);
-        return launched();
+        if constexpr (G > 32) {
+          k_norm_bwd_wide<T, V, G, K><<<unsigned(p.blocks), kThreads, 0, s>>>(
+              in, gamma, g_out, g_in, to, n, int(c), 1.f / float(c), eps);
+          return launched();
+        } else {
+          auto run = [&](auto whole) -> int {
+            auto kern = k_norm_bwd<T, V, G, K, decltype(whole)::value>;
+            constexpr int kMaxDev = 64;
+            static bool attr_set[kMaxDev] = {};  // per device
+            int dev = -1;
+            if (cudaGetDevice(&dev) != cudaSuccess) return int(SMC_ERR_CUDA);
+            if (!(dev >= 0 && dev < kMaxDev && attr_set[dev])) {
+              if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       227 * 1024) != cudaSuccess)
+                return int(SMC_ERR_CUDA);
+              if (dev >= 0 && dev < kMaxDev) attr_set[dev] = true;
+            }
+            kern<<<unsigned(p.blocks), 32 * kRingWarps, p.smem, s>>>(
+                in, gamma, g_out, g_in, to, n, int(c), p.chunk_rows, p.slot_bytes, 1.f / float(c),
+                eps);
+            return launched();
+          };
+          // rows that fill every thread's share are the common ones: no masks
+          if constexpr (V * sizeof(T) >= 8)
+            if (c == G * K * V) return run(std::true_type());
+          return run(std::false_type());
+        }
       });
       if (rc != SMC_OK) return rc;
     }

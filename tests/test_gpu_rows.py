@@ -34,7 +34,8 @@ def _index(n):
 # ---------------------------------------------------------------------------
 NORM_SHAPES = [(1, 1), (5, 2), (1, 64), (3, 7), (424, 16), (1000, 64), (129, 128), (77, 130),
                (50, 255), (64, 512), (33, 515), (20, 1000), (300, 1024), (9, 2048), (5, 4099),
-               (3, 8192), (2, 16384), (40001, 8), (3001, 96)]
+               (3, 8192), (2, 16384), (40001, 8), (3001, 96), (700, 12), (513, 24), (260, 48),
+               (200, 192), (99, 640), (65, 641), (130, 386), (40, 1282), (7, 2560), (1037, 3)]
 
 
 def _norm_inputs(n, c, dt, seed=0):
