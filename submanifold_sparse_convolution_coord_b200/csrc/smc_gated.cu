@@ -39,6 +39,10 @@ namespace smc {
 namespace {
 
 using namespace ptx;
+using rows::add2;
+using rows::dup2;
+using rows::fma2;
+using rows::mul2;
 
 enum Mode { kPre, kPreBwd, kDx, kDw };
 
@@ -86,23 +90,25 @@ struct Seg {
 // the pair's equal share of all tiles' stages.
 template <int MODE>
 struct Walk {
-  int64_t cur, end, step;
   const GemmArgs& a;
+  int64_t cur, end;   // kDw: stages
+  int m, n, dm, dn;   // otherwise: the next tile, and the step from tile to tile
   __device__ __forceinline__ Walk(const GemmArgs& args, int pair) : a(args) {
-    if (MODE == kDw) {
+    if constexpr (MODE == kDw) {
       const int64_t all = int64_t(2) * a.m_tiles * a.n_tiles * a.k_iters;
       cur = pair * all / a.pairs;
       end = (pair + 1) * all / a.pairs;
     } else {
-      cur = pair;
-      end = int64_t(a.m_tiles) * a.n_tiles;
+      m = pair / a.n_tiles;
+      n = pair % a.n_tiles;
+      dm = a.pairs / a.n_tiles;
+      dn = a.pairs % a.n_tiles;
     }
   }
   __device__ __forceinline__ bool next(Seg& g) {
-    if (cur >= end) return false;
-    int tile;
-    if (MODE == kDw) {
-      tile = int(cur / a.k_iters);
+    if constexpr (MODE == kDw) {
+      if (cur >= end) return false;
+      int tile = int(cur / a.k_iters);
       g.k0 = int(cur % a.k_iters);
       g.k1 = int(min(int64_t(a.k_iters), g.k0 + end - cur));
       cur += g.k1 - g.k0;
@@ -112,63 +118,92 @@ struct Walk {
       tile -= g.n * 2 * a.m_tiles;
       g.s = tile / a.m_tiles;
       g.m = tile % a.m_tiles;
-      return true;
     } else {
-      tile = int(cur);
-      g.k0 = 0;
-      g.k1 = a.k_iters;
-      g.s = 0;
-      cur += a.pairs;
+      if (m >= a.m_tiles) return false;
+      g = Seg{m, n, 0, 0, a.k_iters};
+      m += dm;
+      n += dn;
+      if (n >= a.n_tiles) {
+        n -= a.n_tiles;
+        ++m;
+      }
     }
-    g.m = tile / a.n_tiles;
-    g.n = tile % a.n_tiles;
     return true;
   }
 };
 
-// SiLU and its slope through one exponential and one division (both of the
-// fast kind: together within 2^-21 of the value, far inside a 16-bit result's
-// rounding; exp(-v) = inf gives the correct limit 0).
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// exp2 and 1 / x by the hardware's approximations (2 and 1 ulp; results below the
+// normal range become 0, which here only ever adds to 1).
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + exp(-v)); exp(-v) = inf gives the correct limit 0.
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  const float2 x = mul2(v, dup2(-kLog2e));
+  const float2 d = add2(make_float2(exp2_fast(x.x), exp2_fast(x.y)), dup2(1.f));
+  return make_float2(rcp_fast(d.x), rcp_fast(d.y));
+}
 
 // The normal distribution function of v and exp(-v^2 / 2), for GELU and its
 // slope: erfc(x) = t (a1 + a2 t + ... + a5 t^4) exp(-x^2), t = 1 / (1 + p x),
 // x = |v| / sqrt(2) (Hastings, "Approximations for Digital Computers", 1955;
 // Abramowitz and Stegun 7.1.26: within 1.5e-7 of erfc, so within 1e-7 of the
-// function), one exponential and one division where erff takes two polynomials
-// (55,100 rows, 512 -> 2048 bf16: 281 us with erff, TODO us with this).
-__device__ __forceinline__ float2 normal_cdf(float v) {
-  const float e = __expf(-0.5f * v * v);
-  const float t = __fdividef(1.f, fmaf(0.3275911f * 0.7071067811865476f, fabsf(v), 1.f));
-  float q = fmaf(t, 1.061405429f, -1.453152027f);
-  q = fmaf(t, q, 1.421413741f);
-  q = fmaf(t, q, -0.284496736f);
-  q = fmaf(t, q, 0.254829592f);
-  q *= 0.5f * t * e;
-  return make_float2(v > 0.f ? 1.f - q : q, e);
+// function), one exponential and one division where erff takes two polynomials.
+__device__ __forceinline__ float2 normal_cdf2(float2 v, float2& e) {
+  const float2 x = mul2(mul2(v, v), dup2(-0.5f * kLog2e));
+  e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+  constexpr float kP = 0.3275911f * 0.7071067811865476f;
+  const float2 t = make_float2(rcp_fast(fmaf(kP, fabsf(v.x), 1.f)), rcp_fast(fmaf(kP, fabsf(v.y), 1.f)));
+  float2 q = fma2(t, dup2(1.061405429f), dup2(-1.453152027f));
+  q = fma2(t, q, dup2(1.421413741f));
+  q = fma2(t, q, dup2(-0.284496736f));
+  q = fma2(t, q, dup2(0.254829592f));
+  // 0.5 - erfc / 2, with the sign of v, above 0.5
+  q = fma2(mul2(mul2(t, dup2(-0.5f)), e), q, dup2(0.5f));
+  return add2(make_float2(copysignf(q.x, v.x), copysignf(q.y, v.y)), dup2(0.5f));
 }
 
-// The activation's value, and its value and slope.  ACT is a template parameter
-// so that the exponentials of many elements are in flight at once.
+// The activation's value, and its value and slope, of a pair.  Everything that
+// can go in pairs does: the epilogue's instructions have to fit beside the
+// products (see k_gated).
 template <int ACT>
-__device__ __forceinline__ float act_value(float v) {
-  if constexpr (ACT == SMC_ACT_RELU) return fmaxf(v, 0.f);
-  if constexpr (ACT == SMC_ACT_SILU) return v * sigmoid(v);
-  if constexpr (ACT == SMC_ACT_GELU) return v * normal_cdf(v).x;
+__device__ __forceinline__ float2 act_value2(float2 v) {
+  if constexpr (ACT == SMC_ACT_RELU) return make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f));
+  if constexpr (ACT == SMC_ACT_SILU) return mul2(v, sigmoid2(v));
+  if constexpr (ACT == SMC_ACT_GELU) {
+    float2 e;
+    return mul2(v, normal_cdf2(v, e));
+  }
   return v;
 }
 template <int ACT>
-__device__ __forceinline__ float2 act_both(float v) {
-  if constexpr (ACT == SMC_ACT_RELU) return make_float2(fmaxf(v, 0.f), v > 0.f ? 1.f : 0.f);
-  if constexpr (ACT == SMC_ACT_SILU) {
-    const float s = sigmoid(v);
-    return make_float2(v * s, s * (1.f + v * (1.f - s)));
+__device__ __forceinline__ void act_both2(float2 v, float2& value, float2& slope) {
+  if constexpr (ACT == SMC_ACT_RELU) {
+    value = act_value2<ACT>(v);
+    slope = make_float2(v.x > 0.f ? 1.f : 0.f, v.y > 0.f ? 1.f : 0.f);
+  } else if constexpr (ACT == SMC_ACT_SILU) {
+    // s (1 + v (1 - s)) = s + a - a s, a = v s
+    const float2 s = sigmoid2(v);
+    value = mul2(v, s);
+    slope = fma2(mul2(value, s), dup2(-1.f), add2(s, value));
+  } else if constexpr (ACT == SMC_ACT_GELU) {
+    float2 e;
+    const float2 c = normal_cdf2(v, e);
+    value = mul2(v, c);
+    slope = fma2(mul2(v, dup2(0.3989422804014327f)), e, c);
+  } else {
+    value = v;
+    slope = dup2(1.f);
   }
-  if constexpr (ACT == SMC_ACT_GELU) {
-    const float2 c = normal_cdf(v);
-    return make_float2(v * c.x, c.x + v * c.y * 0.3989422804014327f);
-  }
-  return make_float2(v, 1.f);
 }
 
 // x = p[0] + p[1] + p[2] exactly (to 24 bits), each part a bf16 value.  A value
@@ -241,32 +276,26 @@ __device__ __forceinline__ uint32_t value_at(int r, int col) {
 
 // Eight values of a row in the chunk's type, and back.
 template <int DT>
-__device__ __forceinline__ void put8(uint8_t* chunk, int r, int g8, const float (&v)[8]) {
+__device__ __forceinline__ void put8(uint8_t* chunk, int r, int g8, const float2 (&v)[4]) {
   if constexpr (DT == SMC_F32) {
-    *reinterpret_cast<float4*>(chunk + piece<DT>(r, 2 * g8)) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(chunk + piece<DT>(r, 2 * g8)) =
+        make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
     *reinterpret_cast<float4*>(chunk + piece<DT>(r, 2 * g8 + 1)) =
-        make_float4(v[4], v[5], v[6], v[7]);
+        make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   } else {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      w[i] = pack2<DT == SMC_BF16>(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
+      w[i] = pack2<DT == SMC_BF16>(__float_as_uint(v[i].x), __float_as_uint(v[i].y));
     *reinterpret_cast<uint4*>(chunk + piece<DT>(r, g8)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-template <int DT>
-__device__ __forceinline__ void get8(const uint8_t* chunk, int r, int g8, float (&v)[8]) {
-  if constexpr (DT == SMC_F32) {
-    const float4 x = *reinterpret_cast<const float4*>(chunk + piece<DT>(r, 2 * g8));
-    const float4 y = *reinterpret_cast<const float4*>(chunk + piece<DT>(r, 2 * g8 + 1));
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-  } else {
-    using T = typename Elem<DT>::type;
-    uint4 x = *reinterpret_cast<const uint4*>(chunk + piece<DT>(r, g8));
-    const T* t = reinterpret_cast<const T*>(&x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = rows::to_float(t[i]);
-  }
+template <class T>
+__device__ __forceinline__ void unpack8(uint4 x, float2 (&v)[4]) {
+  v[0] = rows::unpack2<T>(x.x);
+  v[1] = rows::unpack2<T>(x.y);
+  v[2] = rows::unpack2<T>(x.z);
+  v[3] = rows::unpack2<T>(x.w);
 }
 
 // Store a warp's staged chunk (32 rows x 32 columns) at (row0, col0) of a
@@ -303,17 +332,14 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* map, bool tma, ui
 template <int DT>
 __device__ __forceinline__ float column_sum(const uint8_t* chunk, int lane) {
   using T = typename Elem<DT>::type;
-  float s0 = 0.f, s1 = 0.f;
+  float2 s = dup2(0.f);
   const int col = (lane & 15) * 2;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    uint32_t w = *reinterpret_cast<const uint32_t*>(chunk + value_at<DT>(2 * i + (lane >> 4), col));
-    const T* t = reinterpret_cast<const T*>(&w);
-    s0 += rows::to_float(t[0]);
-    s1 += rows::to_float(t[1]);
-  }
-  s0 += __shfl_xor_sync(0xffffffffu, s0, 16);
-  s1 += __shfl_xor_sync(0xffffffffu, s1, 16);
+  for (int i = 0; i < 16; ++i)
+    s = add2(s, rows::unpack2<T>(*reinterpret_cast<const uint32_t*>(
+                    chunk + value_at<DT>(2 * i + (lane >> 4), col))));
+  const float s0 = s.x + __shfl_xor_sync(0xffffffffu, s.x, 16);
+  const float s1 = s.y + __shfl_xor_sync(0xffffffffu, s.y, 16);
   // column `lane` is in lane lane / 2
   const float a = __shfl_sync(0xffffffffu, s0, lane >> 1);
   const float b = __shfl_sync(0xffffffffu, s1, lane >> 1);
@@ -364,59 +390,71 @@ struct GateRow {
 template <int MODE, int DT, int ACT, bool BIAS>
 __device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, int g8,
                                       const GateRow& c) {
-  float gg[8], uu[8];
+  float2 gg[4], uu[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    gg[i] = __uint_as_float(gv[i]);
-    uu[i] = __uint_as_float(uv[i]);
+  for (int i = 0; i < 4; ++i) {
+    gg[i] = make_float2(__uint_as_float(gv[2 * i]), __uint_as_float(gv[2 * i + 1]));
+    uu[i] = make_float2(__uint_as_float(uv[2 * i]), __uint_as_float(uv[2 * i + 1]));
   }
+  using T = typename Elem<DT>::type;
   if constexpr (BIAS) {
-    using T = typename Elem<DT>::type;
-    uint4 raw[2][sizeof(T) / 2];
+    float2 b[2][4];
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T) / 2); ++i) {
-      raw[0][i] = reinterpret_cast<const uint4*>(c.bias + g8 * 8 * sizeof(T))[i];
-      raw[1][i] = reinterpret_cast<const uint4*>(c.bias + (32 + g8 * 8) * sizeof(T))[i];
+    for (int k = 0; k < 2; ++k) {
+      const uint8_t* from = c.bias + (32 * k + g8 * 8) * sizeof(T);
+      if constexpr (DT == SMC_F32) {
+        const float4 p = reinterpret_cast<const float4*>(from)[0];
+        const float4 q = reinterpret_cast<const float4*>(from)[1];
+        b[k][0] = make_float2(p.x, p.y), b[k][1] = make_float2(p.z, p.w);
+        b[k][2] = make_float2(q.x, q.y), b[k][3] = make_float2(q.z, q.w);
+      } else {
+        unpack8<T>(*reinterpret_cast<const uint4*>(from), b[k]);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      gg[i] += rows::to_float(reinterpret_cast<const T*>(raw[0])[i]);
-      uu[i] += rows::to_float(reinterpret_cast<const T*>(raw[1])[i]);
+    for (int i = 0; i < 4; ++i) {
+      gg[i] = add2(gg[i], b[0][i]);
+      uu[i] = add2(uu[i], b[1][i]);
     }
   }
   if constexpr (MODE == kPre) {
-    float v[8];
+    float2 v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_value<ACT>(gg[i]) * uu[i];
+    for (int i = 0; i < 4; ++i) v[i] = mul2(act_value2<ACT>(gg[i]), uu[i]);
     put8<DT>(c.slot, c.lane, g8, v);
   } else {
-    float dh[8], G[8], U[8];
+    float2 dh[4], G[4], U[4];
     if constexpr (DT != SMC_F32) {
-      get8<DT>(c.slot, c.lane, g8, dh);
+      unpack8<T>(*reinterpret_cast<const uint4*>(c.slot + piece<DT>(c.lane, g8)), dh);
     } else {
       const int left = c.row_ok ? c.valid - g8 * 8 : 0;
       if (c.dh_vec && left >= 8) {
         const float4 p = *reinterpret_cast<const float4*>(c.dh + g8 * 8);
         const float4 q = *reinterpret_cast<const float4*>(c.dh + g8 * 8 + 4);
-        dh[0] = p.x, dh[1] = p.y, dh[2] = p.z, dh[3] = p.w;
-        dh[4] = q.x, dh[5] = q.y, dh[6] = q.z, dh[7] = q.w;
+        dh[0] = make_float2(p.x, p.y), dh[1] = make_float2(p.z, p.w);
+        dh[2] = make_float2(q.x, q.y), dh[3] = make_float2(q.z, q.w);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dh[i] = i < left ? c.dh[g8 * 8 + i] : 0.f;
+        for (int i = 0; i < 4; ++i)
+          dh[i] = make_float2(2 * i < left ? c.dh[g8 * 8 + 2 * i] : 0.f,
+                              2 * i + 1 < left ? c.dh[g8 * 8 + 2 * i + 1] : 0.f);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = act_both<ACT>(gg[i]);
-      G[i] = dh[i] * uu[i] * f.y;  // dh is 0 in rows and columns that do not exist
-      U[i] = dh[i] * f.x;
+    for (int i = 0; i < 4; ++i) {
+      float2 value, slope;
+      act_both2<ACT>(gg[i], value, slope);
+      G[i] = mul2(mul2(dh[i], uu[i]), slope);  // dh is 0 in rows and columns that do not exist
+      U[i] = mul2(dh[i], value);
     }
     if constexpr (DT != SMC_F32) {
       put8<DT>(c.slot, c.lane, g8, G);
       put8<DT>(c.slot_u, c.lane, g8, U);
     } else {
+      const float gs[8] = {G[0].x, G[0].y, G[1].x, G[1].y, G[2].x, G[2].y, G[3].x, G[3].y};
+      const float us[8] = {U[0].x, U[0].y, U[1].x, U[1].y, U[2].x, U[2].y, U[3].x, U[3].y};
       if (c.db) {
-        const float sg = sum8(G, c.lane), su = sum8(U, c.lane);
+        const float sg = sum8(gs, c.lane), su = sum8(us, c.lane);
         const int col = g8 * 8 + (c.lane >> 2);
         if ((c.lane & 3) == 0 && col < c.valid) {
           c.db[col] = sg;
@@ -430,8 +468,8 @@ __device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, in
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             __nv_bfloat16 lo[3], hi[3];
-            split3(s ? U[2 * i] : G[2 * i], lo);
-            split3(s ? U[2 * i + 1] : G[2 * i + 1], hi);
+            split3(s ? us[2 * i] : gs[2 * i], lo);
+            split3(s ? us[2 * i + 1] : gs[2 * i + 1], hi);
 #pragma unroll
             for (int p = 0; p < 3; ++p)
               w3[p][i] = uint32_t(__bfloat16_as_ushort(lo[p])) |
@@ -779,9 +817,11 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
             __syncwarp();
 #pragma unroll
             for (int g8 = 0; g8 < 4; ++g8) {
-              float f[8];
+              float2 f[4];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[g8 * 8 + i]);
+              for (int i = 0; i < 4; ++i)
+                f[i] = make_float2(__uint_as_float(v[g8 * 8 + 2 * i]),
+                                   __uint_as_float(v[g8 * 8 + 2 * i + 1]));
               put8<DT>(mine, lane, g8, f);
             }
             store_chunk<DT>(&map_out, a.tma_out, mine, a.out, row0, col, a.n, a.C, lane);

@@ -24,6 +24,10 @@
 namespace smc {
 namespace {
 
+using rows::add2;
+using rows::fma2;
+using rows::mul2;
+
 constexpr int kThreads = 256;
 
 // V values of T as one access (V * sizeof(T) <= 16 bytes).
@@ -200,27 +204,6 @@ k_norm(const T* x, const float* __restrict__ gamma, const float* __restrict__ be
 // ---------------------------------------------------------------------------
 // backward, rows of up to a warp
 // ---------------------------------------------------------------------------
-// Pairs of floats: one instruction for two of them (add, multiply, multiply-add
-// on 64-bit register pairs), which matters because the backward does about 14
-// operations per element next to its 6 bytes.
-__device__ __forceinline__ uint64_t bits2(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
-__device__ __forceinline__ float2 float2_of(uint64_t v) { return *reinterpret_cast<float2*>(&v); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return float2_of(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return float2_of(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-  return float2_of(r);
-}
-
 // A lane's share of a row as pairs: value k is vector k / V, element k % V.
 template <class T, int V, int G, int VECS, bool WHOLE>
 struct Share {
