@@ -56,18 +56,20 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kSmemMax = 227 * 1024;
 constexpr uint64_t kAbortDrainNs = 50000000ull;
 
-// The part products of fp32 inputs, smallest first: parts of A and of B.
+// fp32 inputs: the products of parts that are accumulated, smallest first.  A
+// stage holds all three parts of its A and B, so that 96 KB of loads feed six
+// products (with a stage per product it would be 192 KB: 26,214 rows, 128 -> 512:
+// 36.7 us, TODO us so).
 constexpr int kPartPairs = 6;
-__constant__ int8_t kPartA[kPartPairs] = {2, 0, 1, 1, 0, 0};
-__constant__ int8_t kPartB[kPartPairs] = {0, 2, 1, 0, 1, 0};
+__host__ __device__ constexpr int part_a(int q) { return q == 0 ? 2 : (q == 2 || q == 3 ? 1 : 0); }
+__host__ __device__ constexpr int part_b(int q) { return q == 1 ? 2 : (q == 2 || q == 4 ? 1 : 0); }
 
 struct GemmArgs {
   int64_t n;
   int C, H, act;
   int m_tiles, n_tiles;  // kDw: tiles of hidden units per half, of channels
-  int k_chunks, k_iters;  // stages per part product, in all
+  int k_iters;           // stages of a whole tile
   int pairs;             // clusters launched
-  int f32;               // fp32 parts: kPartPairs products instead of one
   const void* bias;      // [2][H] of the element type, or null
   void* out;             // kPre out, kDx dx, kDw dW
   const void* dh;
@@ -237,10 +239,14 @@ struct Elem<SMC_BF16> {
 // tail.
 template <int MODE, int BN, int DT>
 struct Smem {
-  static constexpr int kB = BN / 2 * 128;  // this CTA's half of B
-  static constexpr int kStage = 16384 + kB;
-  static constexpr int kChunkBytes = DT == SMC_F32 ? 4096 : 2048;  // 32 rows x 32 values
-  // chunks of a tile's outputs, dealt to four warps per lane quarter
+  static constexpr int kParts = DT == SMC_F32 ? 3 : 1;
+  static constexpr int kA = 16384;         // this CTA's 128 rows of A, 64 deep, one part
+  static constexpr int kB = BN / 2 * 128;  // its half of B
+  static constexpr int kStage = kParts * (kA + kB);
+  // A staged chunk is 32 rows of 64 bytes: 32 columns, or 16 of fp32.
+  static constexpr int kChunkBytes = 2048;
+  static constexpr int kCols = DT == SMC_F32 ? 16 : 32;
+  // 32-column groups of a tile's outputs, dealt to four warps per lane quarter
   static constexpr int kTileChunks = MODE == kPre || MODE == kPreBwd ? BN / 64 : BN / 32;
   static constexpr int kChunks = (kTileChunks + 3) / 4;  // per warp
   // kPreBwd: dh of this tile (dg takes its place) and of the next, and du;
@@ -249,45 +255,42 @@ struct Smem {
   // from registers.
   static constexpr int kSlots = MODE == kDw ? 0 : (MODE == kPreBwd ? (DT == SMC_F32 ? 0 : 3) : 1);
   static constexpr int kWarpStage = kSlots * kChunkBytes;
-  static constexpr int kBias = 64 * (DT == SMC_F32 ? 4 : 2);  // bias of a warp's chunk
+  static constexpr int kBias = 128;  // bias of a warp's chunk: of g, then of u
   static constexpr int kTailBytes = kEpiWarps * kBias + 512;  // and the barriers
   static constexpr int kStages0 = (kSmemMax - kTailBytes - kEpiWarps * kWarpStage) / kStage;
   static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
   static constexpr int kBytes = kStages * kStage + kEpiWarps * kWarpStage + kTailBytes;
-  static_assert(kStages >= 3, "stages");
+  static_assert(kStages >= 2, "stages");
 };
 
-// Where 16-byte piece `j` of row `r` of a 32-row chunk lies: the TMA's 64-byte
-// swizzle for 16-bit values (64-byte rows), its 128-byte one for fp32.
-template <int DT>
+// Where 16-byte piece `j` of row `r` of a staged chunk lies (the TMA's 64-byte
+// swizzle), and the value in column `col`.
 __device__ __forceinline__ uint32_t piece(int r, int j) {
-  if constexpr (DT == SMC_F32)
-    return r * 128 + ((j ^ (r & 7)) << 4);
-  else
-    return r * 64 + ((j ^ ((r >> 1) & 3)) << 4);
+  return r * 64 + ((j ^ ((r >> 1) & 3)) << 4);
 }
 template <int DT>
 __device__ __forceinline__ uint32_t value_at(int r, int col) {
   if constexpr (DT == SMC_F32)
-    return piece<DT>(r, col >> 2) + (col & 3) * 4;
+    return piece(r, col >> 2) + (col & 3) * 4;
   else
-    return piece<DT>(r, col >> 3) + (col & 7) * 2;
+    return piece(r, col >> 3) + (col & 7) * 2;
 }
 
-// Eight values of a row in the chunk's type, and back.
+// Eight values of a row into the chunk's type: columns 8 g8 .. (fp32: of the
+// chunk's 16).
 template <int DT>
 __device__ __forceinline__ void put8(uint8_t* chunk, int r, int g8, const float2 (&v)[4]) {
   if constexpr (DT == SMC_F32) {
-    *reinterpret_cast<float4*>(chunk + piece<DT>(r, 2 * g8)) =
+    *reinterpret_cast<float4*>(chunk + piece(r, 2 * (g8 & 1))) =
         make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-    *reinterpret_cast<float4*>(chunk + piece<DT>(r, 2 * g8 + 1)) =
+    *reinterpret_cast<float4*>(chunk + piece(r, 2 * (g8 & 1) + 1)) =
         make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   } else {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       w[i] = pack2<DT == SMC_BF16>(__float_as_uint(v[i].x), __float_as_uint(v[i].y));
-    *reinterpret_cast<uint4*>(chunk + piece<DT>(r, g8)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(chunk + piece(r, g8)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 template <class T>
@@ -298,7 +301,7 @@ __device__ __forceinline__ void unpack8(uint4 x, float2 (&v)[4]) {
   v[3] = rows::unpack2<T>(x.w);
 }
 
-// Store a warp's staged chunk (32 rows x 32 columns) at (row0, col0) of a
+// Store a warp's staged chunk at (row0, col0) of a
 // matrix whose rows hold `width` values: one TMA store where the rows are
 // 16-byte multiples (it clips what lies outside), else row by row with a lane
 // per column.  Every lane calls it; the staging may be written again after
@@ -316,13 +319,18 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* map, bool tma, ui
       bulk_commit();
     }
   } else {
+    constexpr int kCols = 64 / int(sizeof(T)), kStep = 32 / kCols;  // kStep rows at a time
     __syncwarp();
-    const int col = col0 + lane;
+    const int r0 = lane / kCols, col = col0 + lane % kCols;
     const int rows_here = int(min(int64_t(32), n - row0));
-    if (col < width)
-      for (int r = 0; r < rows_here; ++r)
-        static_cast<T*>(base)[(row0 + r) * width + col] =
-            *reinterpret_cast<const T*>(chunk + value_at<DT>(r, lane));
+    T* to = static_cast<T*>(base) + (row0 + r0) * width + col;
+    if (col < width) {
+#pragma unroll 8
+      for (int r = 0; r < 32; r += kStep)
+        if (r + r0 < rows_here)
+          to[int64_t(r) * width] =
+              *reinterpret_cast<const T*>(chunk + value_at<DT>(r + r0, lane % kCols));
+    }
     __syncwarp();
   }
 }
@@ -373,7 +381,8 @@ __device__ __forceinline__ float sum8(const float (&v)[8], int lane) {
 
 // What one lane needs for its row of a 32 x 32 chunk of g and u.
 struct GateRow {
-  const uint8_t* bias;  // [2][32] values in shared memory: of g, of u; or null
+  const uint8_t* bias;  // in shared memory, of g, then of u: 32 columns (fp32: the
+                        // half's 16) of each; or null
   uint8_t *slot, *slot_u;
   int lane;
   bool row_ok;
@@ -401,7 +410,8 @@ __device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, in
     float2 b[2][4];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const uint8_t* from = c.bias + (32 * k + g8 * 8) * sizeof(T);
+      const uint8_t* from =
+          c.bias + (DT == SMC_F32 ? 16 * k + (g8 & 1) * 8 : 32 * k + g8 * 8) * sizeof(T);
       if constexpr (DT == SMC_F32) {
         const float4 p = reinterpret_cast<const float4*>(from)[0];
         const float4 q = reinterpret_cast<const float4*>(from)[1];
@@ -425,7 +435,7 @@ __device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, in
   } else {
     float2 dh[4], G[4], U[4];
     if constexpr (DT != SMC_F32) {
-      unpack8<T>(*reinterpret_cast<const uint4*>(c.slot + piece<DT>(c.lane, g8)), dh);
+      unpack8<T>(*reinterpret_cast<const uint4*>(c.slot + piece(c.lane, g8)), dh);
     } else {
       const int left = c.row_ok ? c.valid - g8 * 8 : 0;
       if (c.dh_vec && left >= 8) {
@@ -584,42 +594,40 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
     uint32_t phase = 0;
     bool ok = *abort_flag == 0;
     while (ok && walk.next(g)) {
-      int q = g.k0 / a.k_chunks, kc = g.k0 % a.k_chunks;
       for (int it = g.k0; it < g.k1; ++it) {
         if (!(ok = waits.wait(empty0 + 8 * st, phase ^ 1))) break;
         if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * st, 2 * L::kStage);
         const uint32_t bar = lead_full0 + 8 * st;
-        const uint32_t da = ring0 + st * L::kStage, db = da + 16384;
-        const int pa = a.f32 ? kPartA[q] : 0, pb = a.f32 ? kPartB[q] : 0;
-        const int k = kc * kBK;
-        if constexpr (kPreMode) {
-          tma_load_3d_pair(da, &map_a, k, g.m * 256 + int(rank) * 128, pa, bar);
+        const int k = it * kBK;
 #pragma unroll
-          for (int j = 0; j < BN / 128; ++j)
-            tma_load_3d_pair(db + j * 8192, &map_b, g.n * (BN / 2) + j * 64, k, pb * 2 + int(rank),
-                             bar);
-        } else if constexpr (MODE == kDx) {
-          const int half = a.k_chunks >> 1, s = kc >= half ? 1 : 0;
-          const int h = (kc - s * half) * kBK;
-          tma_load_3d_pair(da, &map_a, h, pa * 2 + s, g.m * 256 + int(rank) * 128, bar);
-          tma_load_3d_pair(db, &map_b, h, g.n * BN + int(rank) * (BN / 2), pb * 2 + s, bar);
-        } else {
+        for (int p = 0; p < L::kParts; ++p) {
+          const uint32_t da = ring0 + st * L::kStage + p * L::kA;
+          const uint32_t db = ring0 + st * L::kStage + L::kParts * L::kA + p * L::kB;
+          if constexpr (kPreMode) {
+            tma_load_3d_pair(da, &map_a, k, g.m * 256 + int(rank) * 128, p, bar);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            tma_load_3d_pair(da + j * 8192, &map_a, g.m * 256 + int(rank) * 128 + j * 64,
-                             pa * 2 + g.s, k, bar);
+            for (int j = 0; j < BN / 128; ++j)
+              tma_load_3d_pair(db + j * 8192, &map_b, g.n * (BN / 2) + j * 64, k, p * 2 + int(rank),
+                               bar);
+          } else if constexpr (MODE == kDx) {
+            const int half = a.k_iters >> 1, s = it >= half ? 1 : 0;
+            const int h = (it - s * half) * kBK;
+            tma_load_3d_pair(da, &map_a, h, p * 2 + s, g.m * 256 + int(rank) * 128, bar);
+            tma_load_3d_pair(db, &map_b, h, g.n * BN + int(rank) * (BN / 2), p * 2 + s, bar);
+          } else {
 #pragma unroll
-          for (int j = 0; j < BN / 128; ++j)
-            tma_load_3d_pair(db + j * 8192, &map_b, g.n * BN + int(rank) * (BN / 2) + j * 64, k, pb,
-                             bar);
+            for (int j = 0; j < 2; ++j)
+              tma_load_3d_pair(da + j * 8192, &map_a, g.m * 256 + int(rank) * 128 + j * 64,
+                               p * 2 + g.s, k, bar);
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j)
+              tma_load_3d_pair(db + j * 8192, &map_b, g.n * BN + int(rank) * (BN / 2) + j * 64, k,
+                               p, bar);
+          }
         }
         if (++st == kStages) {
           st = 0;
           phase ^= 1;
-        }
-        if (++kc == a.k_chunks) {
-          kc = 0;
-          ++q;
         }
       }
     }
@@ -635,14 +643,19 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
       for (int it = g.k0; it < g.k1; ++it) {
         if (!(ok = waits.wait(full0 + 8 * st, phase))) break;
         tc_fence_after();
-        const uint32_t sa = ring0 + st * L::kStage, sb = sa + 16384;
+        const uint32_t stage = ring0 + st * L::kStage;
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k) {
-          const uint64_t da = MODE == kDw ? desc_b_mnmajor(sa + k * 2048, 8192)
-                                          : desc_a_kmajor(sa + k * 32);
-          const uint64_t db = MODE != kDx ? desc_b_mnmajor(sb + k * 2048, 8192)
-                                          : desc_a_kmajor(sb + k * 32);
-          umma_f16_pair(tmem + acc * BN, da, db, kIdesc, it > g.k0 || k > 0);
+        for (int q = 0; q < (L::kParts == 1 ? 1 : kPartPairs); ++q) {
+          const uint32_t sa = stage + (L::kParts == 1 ? 0 : part_a(q)) * L::kA;
+          const uint32_t sb = stage + L::kParts * L::kA + (L::kParts == 1 ? 0 : part_b(q)) * L::kB;
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k) {
+            const uint64_t da = MODE == kDw ? desc_b_mnmajor(sa + k * 2048, 8192)
+                                            : desc_a_kmajor(sa + k * 32);
+            const uint64_t db = MODE != kDx ? desc_b_mnmajor(sb + k * 2048, 8192)
+                                            : desc_a_kmajor(sb + k * 32);
+            umma_f16_pair(tmem + acc * BN, da, db, kIdesc, it > g.k0 || q > 0 || k > 0);
+          }
         }
         umma_commit_pair(empty0 + 8 * st);
         if (++st == kStages) {
@@ -679,8 +692,8 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
     uint32_t dh_phases = 0;  // the parity to wait for next, per slot
     bool ok = *abort_flag == 0;
 
-    // What a tile's epilogue needs from memory, asked for one tile ahead: the
-    // bias of column `lane`, and dh into the staging.
+    // What a tile's epilogue needs from memory, asked for one tile ahead: its bias
+    // values, and dh into the staging.
     T next_bias[2] = {};
     auto live_of = [&](const Seg& t) {
       return hc < BN / 2 && int64_t(t.m) * 256 + my_rows < a.n && t.n * (BN / 2) + hc < a.H;
@@ -688,9 +701,15 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
     auto prefetch = [&](const Seg& t, int slot) {
       if (!kPreMode || !live_of(t)) return;
       const int h = t.n * (BN / 2) + hc;
-      if (a.bias && h + lane < a.H) {
-        next_bias[0] = static_cast<const T*>(a.bias)[h + lane];
-        next_bias[1] = static_cast<const T*>(a.bias)[a.H + h + lane];
+      if (a.bias) {
+        // 16-bit: of g and of u in column `lane`; fp32: of g (lanes 0-15) and u
+        // (16-31) in the first 16 columns, and the second
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int col = h + (DT == SMC_F32 ? 16 * k + (lane & 15) : lane);
+          const int row = DT == SMC_F32 ? lane >> 4 : k;
+          if (col < a.H) next_bias[k] = static_cast<const T*>(a.bias)[row * a.H + col];
+        }
       }
       if constexpr (MODE == kPreBwd && DT != SMC_F32) {
         const int64_t row0 = int64_t(t.m) * 256 + my_rows;
@@ -729,8 +748,11 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
         // one chunk per warp: units h .. h + 31 of the rows row0 .. row0 + 31
         const int h = g.n * (BN / 2) + hc;
         const bool live = live_of(g);
-        bias_w[lane] = next_bias[0];
-        bias_w[32 + lane] = next_bias[1];
+        const T bias[2] = {next_bias[0], next_bias[1]};
+        if constexpr (DT != SMC_F32) {
+          bias_w[lane] = bias[0];
+          bias_w[32 + lane] = bias[1];
+        }
         __syncwarp();
         more = walk.next(gn);
         if (more) prefetch(gn, slot ^ 1);
@@ -774,11 +796,20 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
           }
+          if constexpr (DT == SMC_F32) {
+            __syncwarp();
+            bias_w[lane] = bias[hf];
+            if (hf == 1 && lane == 0) bulk_wait_read<0>();  // the first half's store
+            __syncwarp();
+          }
           gate16<MODE, DT>(gv, uv, hf, a.act, row);
+          if constexpr (MODE == kPre && DT == SMC_F32)
+            if (h + hf * 16 < a.H)
+              store_chunk<DT>(&map_out, a.tma_out, out, a.out, row0, h + hf * 16, a.n, a.H, lane);
         }
-        if constexpr (MODE == kPre) {
+        if constexpr (MODE == kPre && DT != SMC_F32) {
           store_chunk<DT>(&map_out, a.tma_out, out, a.out, row0, h, a.n, a.H, lane);
-        } else if constexpr (DT != SMC_F32) {
+        } else if constexpr (MODE == kPreBwd && DT != SMC_F32) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -813,18 +844,23 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
           if (col >= a.C) continue;
           if constexpr (MODE == kDx) {
             if (row0 >= a.n) continue;
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
 #pragma unroll
-            for (int g8 = 0; g8 < 4; ++g8) {
-              float2 f[4];
+            for (int part = 0; part < 32 / L::kCols; ++part) {
+              if (col + part * L::kCols >= a.C) continue;
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                f[i] = make_float2(__uint_as_float(v[g8 * 8 + 2 * i]),
-                                   __uint_as_float(v[g8 * 8 + 2 * i + 1]));
-              put8<DT>(mine, lane, g8, f);
+              for (int g8 = 0; g8 < L::kCols / 8; ++g8) {
+                const uint32_t* from = v + part * L::kCols + g8 * 8;
+                float2 f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  f[i] = make_float2(__uint_as_float(from[2 * i]), __uint_as_float(from[2 * i + 1]));
+                put8<DT>(mine, lane, g8, f);
+              }
+              store_chunk<DT>(&map_out, a.tma_out, mine, a.out, row0, col + part * L::kCols, a.n,
+                              a.C, lane);
             }
-            store_chunk<DT>(&map_out, a.tma_out, mine, a.out, row0, col, a.n, a.C, lane);
           } else {
             const int64_t h = row0 + lane;
             if (g.k0 == 0 && g.k1 == a.k_iters) {
@@ -865,43 +901,31 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
 }
 
 // dW of the tiles that several pairs worked on: their partial tiles in the
-// order of the pairs.  A block takes 4 columns (input channels) of a tile, and has
-// up to 8 pairs' values of each in flight.
-constexpr int kJoinCols = 4;
-template <class T>
+// order of the pairs.  A block takes one column (input channel) of a tile; a
+// thread has eight pairs' values in flight.  I: an integer that holds a tile
+// count times its stages times the pairs (32 bits divide several times faster).
+template <class T, class I>
 __global__ void __launch_bounds__(256)
 k_join_dw(const float* __restrict__ slots, T* __restrict__ dW, int C, int H, int m_tiles,
           int n_tiles, int k_iters, int pairs, int bn) {
   int tile = blockIdx.x;
-  __shared__ int64_t range[3];  // first and last pair, the first pair's slot
-  if (threadIdx.x == 0) {
-    const int64_t all = int64_t(2) * m_tiles * n_tiles * k_iters;
-    const int64_t i0 = int64_t(tile) * k_iters, i1 = i0 + k_iters;
-    range[0] = ((i0 + 1) * pairs - 1) / all;
-    range[1] = (i1 * pairs - 1) / all;
-    // its second slot if the tile starts its last segment
-    range[2] = 2 * range[0] + (range[0] * all / pairs > i0 ? 0 : 1);
-  }
-  __syncthreads();
-  const int64_t p0 = range[0], p1 = range[1], first = range[2];
+  const int cl = blockIdx.y, c = tile / (2 * m_tiles) * bn + cl;
+  if (c >= C) return;
+  const I all = I(2) * m_tiles * n_tiles * k_iters;
+  const I i0 = I(tile) * k_iters, i1 = i0 + k_iters;
+  const int p0 = int(((i0 + 1) * pairs - 1) / all), p1 = int((i1 * pairs - 1) / all);
   if (p0 == p1) return;  // one pair stored it whole
-  const int cl0 = blockIdx.y * kJoinCols, c0 = tile / (2 * m_tiles) * bn + cl0;
+  // the first pair used its second slot if the tile starts its last segment
+  const int64_t first = 2 * p0 + (p0 * all / pairs > i0 ? 0 : 1);
   tile %= 2 * m_tiles;
   const int64_t s = tile / m_tiles, h = int64_t(tile % m_tiles) * 256 + threadIdx.x;
   if (h >= H) return;
-  const float* from = slots + cl0 * 256 + threadIdx.x;
-  float v[kJoinCols];
-#pragma unroll
-  for (int i = 0; i < kJoinCols; ++i) v[i] = c0 + i < C ? from[first * bn * 256 + i * 256] : 0.f;
+  const float* from = slots + cl * 256 + threadIdx.x;
+  const int64_t slot = int64_t(bn) * 256;
+  float v = from[first * slot];
 #pragma unroll 8
-  for (int64_t p = p0 + 1; p <= p1; ++p) {
-#pragma unroll
-    for (int i = 0; i < kJoinCols; ++i)
-      if (c0 + i < C) v[i] += from[2 * p * bn * 256 + i * 256];
-  }
-#pragma unroll
-  for (int i = 0; i < kJoinCols; ++i)
-    if (c0 + i < C) dW[(s * C + c0 + i) * H + h] = rows::from_float<T>(v[i]);
+  for (int p = p0 + 1; p <= p1; ++p) v += from[2 * p * slot];
+  dW[(s * C + c) * H + h] = rows::from_float<T>(v);
 }
 
 // dbias: the sums over 32 rows, added up in a fixed order.
@@ -922,33 +946,51 @@ k_join_db(const float* __restrict__ part, T* __restrict__ dbias, int64_t blocks,
   }
 }
 
-// src [rows][cols] -> dst [parts][rows][cols_p], 16-bit: the three bf16 parts of
-// fp32 values, or the values themselves, rows padded with zeros to a multiple
-// of 16 bytes.
+// A matrix [rows][cols] and its 16-bit copy [parts][rows][cols_p].
+struct Packing {
+  const void* src;
+  uint16_t* dst;
+  int64_t rows;
+  int cols, cols_p;
+};
+
+// Copies of up to two matrices: the three bf16 parts of fp32 values, or the
+// values themselves, rows padded with zeros to a multiple of 16 bytes.
 template <class T>
-__global__ void __launch_bounds__(256)
-k_parts(const T* __restrict__ src, uint16_t* __restrict__ dst, int64_t nrows, int cols,
-        int cols_p) {
-  const int per_row = cols_p / 8;
-  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < nrows * per_row;
+__global__ void __launch_bounds__(256) k_pack(const Packing one, const Packing two) {
+  const int64_t n1 = one.rows * (one.cols_p / 8), n2 = two.rows * (two.cols_p / 8);
+  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n1 + n2;
        i += int64_t(gridDim.x) * 256) {
-    const int64_t r = i / per_row;
-    const int c = int(i % per_row) * 8;
-    uint16_t v[3][8] = {};
+    const Packing& p = i < n1 ? one : two;
+    const int64_t at = i < n1 ? i : i - n1;
+    const int per_row = p.cols_p / 8;
+    const int64_t r = at >> 32 ? at / per_row : uint32_t(at) / uint32_t(per_row);
+    const int c = int(at - r * per_row) * 8;
+    const T* from = static_cast<const T*>(p.src) + r * p.cols + c;
+    alignas(16) uint16_t v[3][8] = {};
+    alignas(16) T x[8];
+    if (p.cols % 8 == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < cols) {
-        if constexpr (sizeof(T) == 4) {
-          __nv_bfloat16 p[3];
-          split3(src[r * cols + c + j], p);
-          for (int k = 0; k < 3; ++k) v[k][j] = __bfloat16_as_ushort(p[k]);
-        } else {
-          v[0][j] = *reinterpret_cast<const uint16_t*>(&src[r * cols + c + j]);
-        }
+      for (int j = 0; j < int(sizeof(T)) / 2; ++j)
+        reinterpret_cast<uint4*>(x)[j] = reinterpret_cast<const uint4*>(from)[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = c + j < p.cols ? from[j] : rows::from_float<T>(0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        __nv_bfloat16 q[3];
+        split3(x[j], q);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) v[k][j] = __bfloat16_as_ushort(q[k]);
+      } else {
+        v[0][j] = *reinterpret_cast<const uint16_t*>(&x[j]);
       }
+    }
 #pragma unroll
     for (int k = 0; k < (sizeof(T) == 4 ? 3 : 1); ++k)
-      *reinterpret_cast<uint4*>(dst + (k * nrows + r) * cols_p + c) =
+      *reinterpret_cast<uint4*>(p.dst + (k * p.rows + r) * p.cols_p + c) =
           *reinterpret_cast<const uint4*>(v[k]);
   }
 }
@@ -1088,7 +1130,6 @@ struct Run {
     a.C = g.cin;
     a.H = g.hidden;
     a.act = g.act;
-    a.f32 = DT == SMC_F32;
     a.Hp = lay.Hp;
     a.bias = g.bias;
     a.status = g.status;
@@ -1096,13 +1137,13 @@ struct Run {
   }
 
   int pack() const {
-    auto one = [&](const void* src, int64_t off, int64_t nrows, int cols, int cols_p) {
-      const int64_t blocks = parts_up(nrows * (cols_p / 8), 256);
-      k_parts<T><<<unsigned(std::min<int64_t>(blocks, 148 * 16)), 256, 0, s>>>(
-          static_cast<const T*>(src), reinterpret_cast<uint16_t*>(work + off), nrows, cols, cols_p);
-    };
-    if (lay.pack_x) one(g.x, lay.x, g.n, g.cin, lay.Cp);
-    if (lay.pack_w) one(g.W, lay.w, 2 * int64_t(g.cin), g.hidden, lay.Hp);
+    if (!lay.pack_x && !lay.pack_w) return SMC_OK;
+    const Packing px{g.x, reinterpret_cast<uint16_t*>(work + lay.x), lay.pack_x ? g.n : 0, g.cin,
+                     lay.Cp};
+    const Packing pw{g.W, reinterpret_cast<uint16_t*>(work + lay.w),
+                     lay.pack_w ? 2 * int64_t(g.cin) : 0, g.hidden, lay.Hp};
+    const int64_t blocks = parts_up(px.rows * (px.cols_p / 8) + pw.rows * (pw.cols_p / 8), 256);
+    k_pack<T><<<unsigned(std::min<int64_t>(blocks, sm_pairs() * 32)), 256, 0, s>>>(px, pw);
     return cudaGetLastError() == cudaSuccess ? SMC_OK : SMC_ERR_CUDA;
   }
 
@@ -1119,17 +1160,12 @@ struct Run {
     return encode_3d(m, kOp, work + lay.dgu, g.hidden, 2 * lay.parts, g.n, lay.Hp * 2ull,
                      lay.Hp * 4ull * lay.parts, b0, 1, b2);
   }
-  // a caller's [n][width] matrix in 32 x 32 chunks, if its rows allow it
+  // a caller's [n][width] matrix in chunks, if its rows allow it
   bool map_rows(CUtensorMap* m, const void* base, int width, int* usable) const {
     *usable = (int64_t(width) * kE) % 16 == 0;
     if (!*usable) return true;
     return encode_3d(m, DT, base, width, g.n, 1, uint64_t(width) * kE, uint64_t(width) * kE * g.n,
-                     32, 32, 1);
-  }
-
-  void stages(int chunks) {
-    a.k_chunks = chunks;
-    a.k_iters = chunks * (DT == SMC_F32 ? kPartPairs : 1);
+                     64 / kE, 32, 1);
   }
 
   // out = act(g) u, or (dh given) dg and du into the workspace
@@ -1138,7 +1174,7 @@ struct Run {
     const int bn = g.hidden > 64 ? 256 : 128;
     a.m_tiles = int(parts_up(g.n, 256));
     a.n_tiles = int(parts_up(g.hidden, bn / 2));
-    stages(int(parts_up(g.cin, kBK)));
+    a.k_iters = int(parts_up(g.cin, kBK));
     a.pairs = int(std::min<int64_t>(sm_pairs(), int64_t(a.m_tiles) * a.n_tiles));
     if (!map_x(&ma, kBK, 128) || !map_w(&mb, kBK, kBK)) return SMC_ERR_CUDA;
     if (!dh) {
@@ -1158,7 +1194,7 @@ struct Run {
     const int bn = Layout::bn_for(g.cin);
     a.m_tiles = int(parts_up(g.n, 256));
     a.n_tiles = int(parts_up(g.cin, bn));
-    stages(2 * int(parts_up(g.hidden, kBK)));
+    a.k_iters = 2 * int(parts_up(g.hidden, kBK));
     a.pairs = int(std::min<int64_t>(sm_pairs(), int64_t(a.m_tiles) * a.n_tiles));
     a.out = dx;
     if (!map_dgu(&ma, kBK, 128) || !map_w(&mb, kBK, bn / 2) ||
@@ -1172,7 +1208,7 @@ struct Run {
     const int bn = Layout::bn_for(g.cin);
     a.m_tiles = int(parts_up(g.hidden, 256));
     a.n_tiles = int(parts_up(g.cin, bn));
-    stages(int(parts_up(g.n, kBK)));
+    a.k_iters = int(parts_up(g.n, kBK));
     const int tiles = 2 * a.m_tiles * a.n_tiles;
     a.pairs = int(std::min<int64_t>(sm_pairs(), int64_t(tiles) * a.k_iters));
     a.out = dW;
@@ -1180,8 +1216,11 @@ struct Run {
     if (!map_dgu(&ma, kBK, kBK) || !map_x(&mb, kBK, kBK)) return SMC_ERR_CUDA;
     const int rc = launch_bn<kDw, DT>(bn, ma, mb, mo, md, a, s);
     if (rc != SMC_OK) return rc;
-    k_join_dw<T><<<dim3(tiles, bn / kJoinCols), 256, 0, s>>>(a.slots, static_cast<T*>(dW), g.cin, g.hidden,
-                                                     a.m_tiles, a.n_tiles, a.k_iters, a.pairs, bn);
+    auto join = (int64_t(tiles) * a.k_iters + 1) * a.pairs < (int64_t(1) << 32)
+                    ? k_join_dw<T, uint32_t>
+                    : k_join_dw<T, uint64_t>;
+    join<<<dim3(tiles, bn), 256, 0, s>>>(a.slots, static_cast<T*>(dW), g.cin, g.hidden, a.m_tiles,
+                                         a.n_tiles, a.k_iters, a.pairs, bn);
     return cudaGetLastError() == cudaSuccess ? SMC_OK : SMC_ERR_CUDA;
   }
 
