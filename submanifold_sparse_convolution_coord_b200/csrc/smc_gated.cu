@@ -385,28 +385,26 @@ struct GateRow {
                         // half's 16) of each; or null
   uint8_t *slot, *slot_u;
   int lane;
-  bool row_ok;
-  const float* dh;  // fp32, kPreBwd: the row's dh (dh_vec: 16-byte aligned)
-  bool dh_vec;
-  uint16_t* dgu;  // fp32, kPreBwd: where the row's dg parts go
+  // fp32, kPreBwd:
+  const float* dh;  // the row's dh (dh_vec: 16-byte aligned)
+  bool dh_vec, row_ok;
+  uint16_t* dgu;  // where the row's dg parts go
   int Hp, valid;  // valid: columns of the chunk that exist
-  float* db;      // fp32, kPreBwd: the chunk's column sums of dg, or null
+  float* db;      // the chunk's column sums of dg, or null
   int64_t db_u;   // from there to those of du
 };
 
-// Columns g8 * 8 .. + 7 of it.  kPre: act(g) u into `slot`; kPreBwd: dh from
-// `slot`, dg in its place and du into `slot_u` (fp32: their parts to dgu).
-template <int MODE, int DT, int ACT, bool BIAS>
-__device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, int g8,
-                                      const GateRow& c) {
-  float2 gg[4], uu[4];
+// Columns g8 * 8 .. + 7 of g and u: accumulators and bias.
+template <int DT, bool BIAS>
+__device__ __forceinline__ void biased8(const uint32_t* gv, const uint32_t* uv, int g8,
+                                        const GateRow& c, float2 (&gg)[4], float2 (&uu)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     gg[i] = make_float2(__uint_as_float(gv[2 * i]), __uint_as_float(gv[2 * i + 1]));
     uu[i] = make_float2(__uint_as_float(uv[2 * i]), __uint_as_float(uv[2 * i + 1]));
   }
-  using T = typename Elem<DT>::type;
   if constexpr (BIAS) {
+    using T = typename Elem<DT>::type;
     float2 b[2][4];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -427,29 +425,24 @@ __device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, in
       uu[i] = add2(uu[i], b[1][i]);
     }
   }
+}
+
+// kPre: act(g) u into `slot`; kPreBwd, 16-bit: dh from `slot`, dg in its place
+// and du into `slot_u`.
+template <int MODE, int DT, int ACT, bool BIAS>
+__device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, int g8,
+                                      const GateRow& c) {
+  float2 gg[4], uu[4];
+  biased8<DT, BIAS>(gv, uv, g8, c, gg, uu);
   if constexpr (MODE == kPre) {
     float2 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(act_value2<ACT>(gg[i]), uu[i]);
     put8<DT>(c.slot, c.lane, g8, v);
   } else {
+    using T = typename Elem<DT>::type;
     float2 dh[4], G[4], U[4];
-    if constexpr (DT != SMC_F32) {
-      unpack8<T>(*reinterpret_cast<const uint4*>(c.slot + piece(c.lane, g8)), dh);
-    } else {
-      const int left = c.row_ok ? c.valid - g8 * 8 : 0;
-      if (c.dh_vec && left >= 8) {
-        const float4 p = *reinterpret_cast<const float4*>(c.dh + g8 * 8);
-        const float4 q = *reinterpret_cast<const float4*>(c.dh + g8 * 8 + 4);
-        dh[0] = make_float2(p.x, p.y), dh[1] = make_float2(p.z, p.w);
-        dh[2] = make_float2(q.x, q.y), dh[3] = make_float2(q.z, q.w);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dh[i] = make_float2(2 * i < left ? c.dh[g8 * 8 + 2 * i] : 0.f,
-                              2 * i + 1 < left ? c.dh[g8 * 8 + 2 * i + 1] : 0.f);
-      }
-    }
+    unpack8<T>(*reinterpret_cast<const uint4*>(c.slot + piece(c.lane, g8)), dh);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 value, slope;
@@ -457,40 +450,69 @@ __device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, in
       G[i] = mul2(mul2(dh[i], uu[i]), slope);  // dh is 0 in rows and columns that do not exist
       U[i] = mul2(dh[i], value);
     }
-    if constexpr (DT != SMC_F32) {
-      put8<DT>(c.slot, c.lane, g8, G);
-      put8<DT>(c.slot_u, c.lane, g8, U);
-    } else {
-      const float gs[8] = {G[0].x, G[0].y, G[1].x, G[1].y, G[2].x, G[2].y, G[3].x, G[3].y};
-      const float us[8] = {U[0].x, U[0].y, U[1].x, U[1].y, U[2].x, U[2].y, U[3].x, U[3].y};
+    put8<DT>(c.slot, c.lane, g8, G);
+    put8<DT>(c.slot_u, c.lane, g8, U);
+  }
+}
+
+// Eight words as one 32-byte store: a whole sector.
+__device__ __forceinline__ void store_32(void* to, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// kPreBwd, fp32, sixteen columns: the parts of dg, then of du (the activation
+// is taken twice rather than both held), 32 bytes of a row at a time, and the
+// column sums.
+template <int ACT, bool BIAS>
+__device__ __forceinline__ void gate16_parts(const uint32_t* gv, const uint32_t* uv, int hf,
+                                             const GateRow& c) {
+  const int left = c.row_ok ? c.valid - hf * 16 : 0;
+  float dh[16];
+  if (c.dh_vec && left >= 16) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 p = *reinterpret_cast<const float4*>(c.dh + hf * 16 + i);
+      dh[i] = p.x, dh[i + 1] = p.y, dh[i + 2] = p.z, dh[i + 3] = p.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dh[i] = i < left ? c.dh[hf * 16 + i] : 0.f;
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    uint32_t parts[3][8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float2 gg[4], uu[4];
+      float v[8];
+      biased8<SMC_F32, BIAS>(gv + 8 * j, uv + 8 * j, j, c, gg, uu);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 value, slope;
+        act_both2<ACT>(gg[i], value, slope);
+        const float2 d = make_float2(dh[8 * j + 2 * i], dh[8 * j + 2 * i + 1]);
+        const float2 r = s == 0 ? mul2(mul2(d, uu[i]), slope) : mul2(d, value);
+        v[2 * i] = r.x;
+        v[2 * i + 1] = r.y;
+        __nv_bfloat16 lo[3], hi[3];
+        split3(r.x, lo);
+        split3(r.y, hi);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+          parts[p][4 * j + i] = uint32_t(__bfloat16_as_ushort(lo[p])) |
+                                uint32_t(__bfloat16_as_ushort(hi[p])) << 16;
+      }
       if (c.db) {
-        const float sg = sum8(gs, c.lane), su = sum8(us, c.lane);
-        const int col = g8 * 8 + (c.lane >> 2);
-        if ((c.lane & 3) == 0 && col < c.valid) {
-          c.db[col] = sg;
-          c.db[c.db_u + col] = su;
-        }
+        const float sum = sum8(v, c.lane);
+        const int col = hf * 16 + j * 8 + (c.lane >> 2);
+        if ((c.lane & 3) == 0 && col < c.valid) c.db[s * c.db_u + col] = sum;
       }
-      if (c.row_ok && g8 * 8 < c.valid) {
+    }
+    if (left > 0) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          uint32_t w3[3][4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            __nv_bfloat16 lo[3], hi[3];
-            split3(s ? us[2 * i] : gs[2 * i], lo);
-            split3(s ? us[2 * i + 1] : gs[2 * i + 1], hi);
-#pragma unroll
-            for (int p = 0; p < 3; ++p)
-              w3[p][i] = uint32_t(__bfloat16_as_ushort(lo[p])) |
-                         uint32_t(__bfloat16_as_ushort(hi[p])) << 16;
-          }
-#pragma unroll
-          for (int p = 0; p < 3; ++p)
-            *reinterpret_cast<uint4*>(c.dgu + (p * 2 + s) * c.Hp + g8 * 8) =
-                make_uint4(w3[p][0], w3[p][1], w3[p][2], w3[p][3]);
-        }
-      }
+      for (int p = 0; p < 3; ++p) store_32(c.dgu + (p * 2 + s) * c.Hp + hf * 16, parts[p]);
     }
   }
 }
@@ -501,6 +523,8 @@ template <int MODE, int DT>
 __device__ __forceinline__ void gate16(const uint32_t (&gv)[16], const uint32_t (&uv)[16], int hf,
                                        int act, const GateRow& c) {
   auto go = [&](auto a, auto b) {
+    if constexpr (MODE == kPreBwd && DT == SMC_F32)
+      return gate16_parts<decltype(a)::value, decltype(b)::value>(gv, uv, hf, c);
     gate8<MODE, DT, decltype(a)::value, decltype(b)::value>(gv, uv, 2 * hf, c);
     gate8<MODE, DT, decltype(a)::value, decltype(b)::value>(gv + 8, uv + 8, 2 * hf + 1, c);
   };
@@ -780,11 +804,17 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
         uint8_t* out_u = mine + 2 * L::kChunkBytes;  // kPreBwd, 16-bit
         const int64_t block = (int64_t(g.m) * 2 + rank) * 4 + quarter;
         float* db = MODE == kPreBwd && a.db_part ? a.db_part + block * 2 * a.H + h : nullptr;
-        const GateRow row{a.bias ? reinterpret_cast<const uint8_t*>(bias_w) : nullptr, out, out_u,
-                          lane, row0 + lane < a.n,
-                          static_cast<const float*>(a.dh) + (row0 + lane) * a.H + h,
-                          a.tma_dh != 0, a.dgu + (row0 + lane) * 6 * a.Hp + h, a.Hp,
-                          a.H - h, db, a.H};
+        GateRow row{a.bias ? reinterpret_cast<const uint8_t*>(bias_w) : nullptr, out, out_u, lane};
+        if constexpr (MODE == kPreBwd && DT == SMC_F32) {
+          row.dh = static_cast<const float*>(a.dh) + (row0 + lane) * a.H + h;
+          row.dh_vec = a.tma_dh != 0;
+          row.row_ok = row0 + lane < a.n;
+          row.dgu = a.dgu + (row0 + lane) * 6 * a.Hp + h;
+          row.Hp = a.Hp;
+          row.valid = a.H - h;
+          row.db = db;
+          row.db_u = a.H;
+        }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t gv[16], uv[16];
@@ -901,15 +931,16 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
 }
 
 // dW of the tiles that several pairs worked on: their partial tiles in the
-// order of the pairs.  A block takes one column (input channel) of a tile; a
-// thread has eight pairs' values in flight.  I: an integer that holds a tile
-// count times its stages times the pairs (32 bits divide several times faster).
-template <class T, class I>
+// order of the pairs.  A block takes COLS columns (input channels) of a tile; a
+// thread has up to eight pairs' values of each in flight.  I: an integer that
+// holds the tiles times their stages times the pairs (32 bits divide several
+// times faster).
+template <class T, class I, int COLS>
 __global__ void __launch_bounds__(256)
 k_join_dw(const float* __restrict__ slots, T* __restrict__ dW, int C, int H, int m_tiles,
           int n_tiles, int k_iters, int pairs, int bn) {
   int tile = blockIdx.x;
-  const int cl = blockIdx.y, c = tile / (2 * m_tiles) * bn + cl;
+  const int cl = blockIdx.y * COLS, c = tile / (2 * m_tiles) * bn + cl;
   if (c >= C) return;
   const I all = I(2) * m_tiles * n_tiles * k_iters;
   const I i0 = I(tile) * k_iters, i1 = i0 + k_iters;
@@ -922,10 +953,17 @@ k_join_dw(const float* __restrict__ slots, T* __restrict__ dW, int C, int H, int
   if (h >= H) return;
   const float* from = slots + cl * 256 + threadIdx.x;
   const int64_t slot = int64_t(bn) * 256;
-  float v = from[first * slot];
+  float v[COLS];
+#pragma unroll
+  for (int i = 0; i < COLS; ++i) v[i] = from[first * slot + i * 256];
 #pragma unroll 8
-  for (int p = p0 + 1; p <= p1; ++p) v += from[2 * p * slot];
-  dW[(s * C + c) * H + h] = rows::from_float<T>(v);
+  for (int p = p0 + 1; p <= p1; ++p) {
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) v[i] += from[2 * p * slot + i * 256];
+  }
+#pragma unroll
+  for (int i = 0; i < COLS; ++i)
+    if (c + i < C) dW[(s * C + c + i) * H + h] = rows::from_float<T>(v[i]);
 }
 
 // dbias: the sums over 32 rows, added up in a fixed order.
@@ -1062,7 +1100,7 @@ struct Layout {
     const bool f32 = dtype == SMC_F32;
     parts = f32 ? 3 : 1;
     Cp = int(up(C, 8));
-    Hp = int(up(H, 8));
+    Hp = int(up(H, f32 ? 16 : 8));  // fp32: dg and du are written in 32-byte pieces
     pack_x = f32 || C % 8 != 0;
     pack_w = f32 || H % 8 != 0;
     int64_t at = 0;
@@ -1076,7 +1114,7 @@ struct Layout {
     dgu = take(backward ? n * 2 * parts * Hp * 2 : 0);
     db = take(backward ? parts_up(n, 256) * 8 * 2 * H * 4 : 0);
     slots = take(backward ? int64_t(2) * sm_pairs() * bn_for(C) * 256 * 4 : 0);
-    total = at;
+    total = at > 0 ? at + 256 : 0;  // offsets are from a 256-byte boundary
   }
   // Columns of a dx or dW tile.
   static int bn_for(int C) { return C > 128 ? 256 : 128; }
@@ -1123,7 +1161,8 @@ struct Run {
 
   Run(const GatedCall& call, bool backward, cudaStream_t stream)
       : g(call), lay(call.n, call.cin, call.hidden, call.dtype, backward), s(stream),
-        work(static_cast<uint8_t*>(call.workspace)) {
+        work(reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(call.workspace) + 255) &
+                                        ~uintptr_t(255))) {
     x = lay.pack_x ? work + lay.x : g.x;
     W = lay.pack_w ? work + lay.w : g.W;
     a.n = g.n;
@@ -1216,11 +1255,14 @@ struct Run {
     if (!map_dgu(&ma, kBK, kBK) || !map_x(&mb, kBK, kBK)) return SMC_ERR_CUDA;
     const int rc = launch_bn<kDw, DT>(bn, ma, mb, mo, md, a, s);
     if (rc != SMC_OK) return rc;
+    // one column per block while the blocks are few (two tiles of 37 parts each:
+    // 5 us, with four 14.5), else four (32 tiles: 12 us, with one 28)
+    const bool few = int64_t(tiles) * bn < 4096;
     auto join = (int64_t(tiles) * a.k_iters + 1) * a.pairs < (int64_t(1) << 32)
-                    ? k_join_dw<T, uint32_t>
-                    : k_join_dw<T, uint64_t>;
-    join<<<dim3(tiles, bn), 256, 0, s>>>(a.slots, static_cast<T*>(dW), g.cin, g.hidden, a.m_tiles,
-                                         a.n_tiles, a.k_iters, a.pairs, bn);
+                    ? (few ? k_join_dw<T, uint32_t, 1> : k_join_dw<T, uint32_t, 4>)
+                    : (few ? k_join_dw<T, uint64_t, 1> : k_join_dw<T, uint64_t, 4>);
+    join<<<dim3(tiles, few ? bn : bn / 4), 256, 0, s>>>(
+        a.slots, static_cast<T*>(dW), g.cin, g.hidden, a.m_tiles, a.n_tiles, a.k_iters, a.pairs, bn);
     return cudaGetLastError() == cudaSuccess ? SMC_OK : SMC_ERR_CUDA;
   }
 
