@@ -56,7 +56,13 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kSmemMax = 227 * 1024;
 constexpr uint64_t kAbortDrainNs = 50000000ull;
 
-// fp32 inputs: the products of parts that are accumulated, smallest first.  A
+// fp32 inputs: an accumulation in tensor memory cuts what falls below the sum's
+// last bit instead of rounding it, so its error grows with the number of steps
+// (2.3e-8 of the sum per 16-deep step was measured); each stage is therefore
+// accumulated on its own (24 steps) and the epilogue's warps add the stages up
+// in registers, rounding.
+//
+// The products of parts that are accumulated, smallest first.  A
 // stage holds all three parts of its A and B, so that 96 KB of loads feed six
 // products (with a stage per product it would be 192 KB: 26,214 rows, 128 -> 512:
 // 36.7 us, TODO us so).
@@ -335,25 +341,6 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* map, bool tma, ui
   }
 }
 
-// Sum over a staged 16-bit chunk's 32 rows, for column `lane`: half a warp
-// takes the even rows and half the odd ones, two columns a lane.
-template <int DT>
-__device__ __forceinline__ float column_sum(const uint8_t* chunk, int lane) {
-  using T = typename Elem<DT>::type;
-  float2 s = dup2(0.f);
-  const int col = (lane & 15) * 2;
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    s = add2(s, rows::unpack2<T>(*reinterpret_cast<const uint32_t*>(
-                    chunk + value_at<DT>(2 * i + (lane >> 4), col))));
-  const float s0 = s.x + __shfl_xor_sync(0xffffffffu, s.x, 16);
-  const float s1 = s.y + __shfl_xor_sync(0xffffffffu, s.y, 16);
-  // column `lane` is in lane lane / 2
-  const float a = __shfl_sync(0xffffffffu, s0, lane >> 1);
-  const float b = __shfl_sync(0xffffffffu, s1, lane >> 1);
-  return lane & 1 ? b : a;
-}
-
 // Sums over the warp's lanes of eight values each; lane l ends with the sum of
 // value l / 4 (exchanges that halve the values three times, then two plain steps).
 __device__ __forceinline__ float sum8(const float (&v)[8], int lane) {
@@ -389,10 +376,19 @@ struct GateRow {
   const float* dh;  // the row's dh (dh_vec: 16-byte aligned)
   bool dh_vec, row_ok;
   uint16_t* dgu;  // where the row's dg parts go
-  int Hp, valid;  // valid: columns of the chunk that exist
-  float* db;      // the chunk's column sums of dg, or null
-  int64_t db_u;   // from there to those of du
+  int Hp;
+  // kPreBwd:
+  int valid;     // columns of the chunk that exist
+  float* db;     // the chunk's column sums of dg, or null
+  int64_t db_u;  // from there to those of du
 };
+
+// Column sums of eight columns of dg (s = 0) or du before they are rounded.
+__device__ __forceinline__ void sum_columns(const float (&v)[8], int s, int g8, const GateRow& c) {
+  const float sum = sum8(v, c.lane);
+  const int col = g8 * 8 + (c.lane >> 2);
+  if ((c.lane & 3) == 0 && col < c.valid) c.db[s * c.db_u + col] = sum;
+}
 
 // Columns g8 * 8 .. + 7 of g and u: accumulators and bias.
 template <int DT, bool BIAS>
@@ -452,6 +448,12 @@ __device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, in
     }
     put8<DT>(c.slot, c.lane, g8, G);
     put8<DT>(c.slot_u, c.lane, g8, U);
+    if (c.db) {
+      const float g[8] = {G[0].x, G[0].y, G[1].x, G[1].y, G[2].x, G[2].y, G[3].x, G[3].y};
+      const float u[8] = {U[0].x, U[0].y, U[1].x, U[1].y, U[2].x, U[2].y, U[3].x, U[3].y};
+      sum_columns(g, 0, g8, c);
+      sum_columns(u, 1, g8, c);
+    }
   }
 }
 
@@ -504,11 +506,7 @@ __device__ __forceinline__ void gate16_parts(const uint32_t* gv, const uint32_t*
           parts[p][4 * j + i] = uint32_t(__bfloat16_as_ushort(lo[p])) |
                                 uint32_t(__bfloat16_as_ushort(hi[p])) << 16;
       }
-      if (c.db) {
-        const float sum = sum8(v, c.lane);
-        const int col = hf * 16 + j * 8 + (c.lane >> 2);
-        if ((c.lane & 3) == 0 && col < c.valid) c.db[s * c.db_u + col] = sum;
-      }
+      if (c.db) sum_columns(v, s, 2 * hf + j, c);
     }
     if (left > 0) {
 #pragma unroll
@@ -556,6 +554,8 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   constexpr int kStages = L::kStages;
   constexpr bool kPreMode = MODE == kPre || MODE == kPreBwd;
   constexpr uint32_t kTmemCols = 2 * BN;
+  constexpr bool kStageSums = DT == SMC_F32;
+  constexpr int kSums = kStageSums ? (kPreMode ? 2 : L::kChunks) * 32 : 1;
   // M = 256 over the pair; A is MN-major in kDw, B in all modes but kDx
   constexpr uint32_t kIdesc = (1u << 4) | ((DT != SMC_F16 ? 1u : 0u) << 7) |
                               ((DT != SMC_F16 ? 1u : 0u) << 10) | ((MODE == kDw ? 1u : 0u) << 15) |
@@ -661,10 +661,13 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
     uint32_t phase = 0;
     bool ok = *abort_flag == 0;
     while (ok && walk.next(g)) {
-      const int acc = seg & 1;
-      if (!(ok = waits.wait(tempty0 + 8 * acc, ((seg >> 1) & 1) ^ 1))) break;
-      tc_fence_after();
+      int acc = 0;
       for (int it = g.k0; it < g.k1; ++it) {
+        if (kStageSums || it == g.k0) {  // a new accumulation
+          acc = seg & 1;
+          if (!(ok = waits.wait(tempty0 + 8 * acc, ((seg >> 1) & 1) ^ 1))) break;
+          ++seg;
+        }
         if (!(ok = waits.wait(full0 + 8 * st, phase))) break;
         tc_fence_after();
         const uint32_t stage = ring0 + st * L::kStage;
@@ -678,18 +681,17 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
                                             : desc_a_kmajor(sa + k * 32);
             const uint64_t db = MODE != kDx ? desc_b_mnmajor(sb + k * 2048, 8192)
                                             : desc_a_kmajor(sb + k * 32);
-            umma_f16_pair(tmem + acc * BN, da, db, kIdesc, it > g.k0 || q > 0 || k > 0);
+            umma_f16_pair(tmem + acc * BN, da, db, kIdesc,
+                          (!kStageSums && it > g.k0) || q > 0 || k > 0);
           }
         }
         umma_commit_pair(empty0 + 8 * st);
+        if (kStageSums || it + 1 == g.k1) umma_commit_pair(tfull0 + 8 * acc);
         if (++st == kStages) {
           st = 0;
           phase ^= 1;
         }
       }
-      if (!ok) break;
-      umma_commit_pair(tfull0 + 8 * acc);
-      ++seg;
     }
     if (!ok) {  // let what was issued finish before memory is released
       umma_commit_pair(drain);
@@ -762,12 +764,46 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
     Seg gn;
     bool more = ok && walk.next(g);
     if (more) prefetch(g, 0);
-    for (; ok && more; g = gn) {
-      const int acc = seg & 1, slot = seg & 1;
-      const uint32_t parity = (seg >> 1) & 1;
-      const uint32_t d = lanes + acc * BN;
+    for (int turn = 0; ok && more; g = gn, ++turn) {
+      const int slot = turn & 1;
       const int64_t row0 = int64_t(g.m) * 256 + my_rows;
-      ++seg;
+      // The accumulation that is next, from the warp's lanes of tensor memory.
+      uint32_t d = 0;
+      int acc = 0;
+      auto next_sums = [&]() {
+        acc = seg & 1;
+        d = lanes + acc * BN;
+        const bool got = waits.wait(tfull0 + 8 * acc, (seg >> 1) & 1);
+        tc_fence_after();
+        ++seg;
+        return got;
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+      };
+      // fp32: the stages' sums, added up.  Value i is column column_of(i / 32) + i % 32.
+      float sums[kSums];
+      auto add_stages = [&](bool live, auto column_of) {
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) sums[i] = 0.f;
+        for (int it = g.k0; it < g.k1; ++it) {
+          if (!next_sums()) return false;
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < kSums; i += 16) {
+              uint32_t v[16];
+              tmem_ld_x16_async(d + column_of(i / 32) + i % 32, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sums[i + j] += __uint_as_float(v[j]);
+            }
+          }
+          release();
+        }
+        return true;
+      };
       if constexpr (kPreMode) {
         // one chunk per warp: units h .. h + 31 of the rows row0 .. row0 + 31
         const int h = g.n * (BN / 2) + hc;
@@ -780,12 +816,14 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
         __syncwarp();
         more = walk.next(gn);
         if (more) prefetch(gn, slot ^ 1);
-        if (!(ok = waits.wait(tfull0 + 8 * acc, parity))) break;
-        tc_fence_after();
+        if constexpr (kStageSums) {
+          ok = add_stages(live, [&](int k) { return k * (BN / 2) + hc; });
+          if (!ok) break;
+        } else {
+          if (!(ok = next_sums())) break;
+        }
         if (!live) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+          if (!kStageSums) release();
           continue;
         }
         uint8_t* out = mine;  // kPre: act(g) u; kPreBwd: dh, then dg
@@ -811,6 +849,8 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
           row.row_ok = row0 + lane < a.n;
           row.dgu = a.dgu + (row0 + lane) * 6 * a.Hp + h;
           row.Hp = a.Hp;
+        }
+        if constexpr (MODE == kPreBwd) {
           row.valid = a.H - h;
           row.db = db;
           row.db_u = a.H;
@@ -818,13 +858,17 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t gv[16], uv[16];
-          tmem_ld_x16_async(d + hc + hf * 16, gv);
-          tmem_ld_x16_async(d + BN / 2 + hc + hf * 16, uv);
-          tmem_ld_wait();
-          if (hf == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+          if constexpr (kStageSums) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              gv[i] = __float_as_uint(sums[hf * 16 + i]);
+              uv[i] = __float_as_uint(sums[32 + hf * 16 + i]);
+            }
+          } else {
+            tmem_ld_x16_async(d + hc + hf * 16, gv);
+            tmem_ld_x16_async(d + BN / 2 + hc + hf * 16, uv);
+            tmem_ld_wait();
+            if (hf == 1) release();
           }
           if constexpr (DT == SMC_F32) {
             __syncwarp();
@@ -847,29 +891,26 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
             tma_store_3d(&map_out, smem_addr(out_u), h, 1, int(row0));
             bulk_commit();
           }
-          if (db) {
-            const float sg = column_sum<DT>(out, lane), su = column_sum<DT>(out_u, lane);
-            if (h + lane < a.H) {
-              db[lane] = sg;
-              db[a.H + lane] = su;
-            }
-          }
         }
         __syncwarp();
       } else {
         more = walk.next(gn);
-        if (!(ok = waits.wait(tfull0 + 8 * acc, parity))) break;
-        tc_fence_after();
-#pragma unroll 1
+        if constexpr (kStageSums)
+          ok = add_stages(true, [&](int k) { return (group * L::kChunks + k) * 32; });
+        else
+          ok = next_sums();
+        if (!ok) break;
+#pragma unroll
         for (int c = 0; c < L::kChunks; ++c) {
           const int cc = (group * L::kChunks + c) * 32, col = g.n * BN + cc;
           uint32_t v[32];
-          tmem_ld_x32_async(d + cc, v);
-          tmem_ld_wait();
-          if (c == L::kChunks - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+          if constexpr (kStageSums) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sums[c * 32 + i]);
+          } else {
+            tmem_ld_x32_async(d + cc, v);
+            tmem_ld_wait();
+            if (c == L::kChunks - 1) release();
           }
           if (col >= a.C) continue;
           if constexpr (MODE == kDx) {
