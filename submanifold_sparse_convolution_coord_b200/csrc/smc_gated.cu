@@ -606,6 +606,8 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   __syncwarp();
   cluster_sync();
   tc_fence_after();
+  rows::let_next_start();
+  rows::after_previous();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const Waits waits{abort_flag, a.status, a.wait_ns};
   Walk<MODE> walk(a, pair);
@@ -980,6 +982,8 @@ template <class T, class I, int COLS>
 __global__ void __launch_bounds__(256)
 k_join_dw(const float* __restrict__ slots, T* __restrict__ dW, int C, int H, int m_tiles,
           int n_tiles, int k_iters, int pairs, int bn) {
+  rows::let_next_start();
+  rows::after_previous();
   int tile = blockIdx.x;
   const int cl = blockIdx.y * COLS, c = tile / (2 * m_tiles) * bn + cl;
   if (c >= C) return;
@@ -1012,6 +1016,8 @@ template <class T>
 __global__ void __launch_bounds__(1024)
 k_join_db(const float* __restrict__ part, T* __restrict__ dbias, int64_t blocks, int H2) {
   __shared__ float sums[32][33];
+  rows::let_next_start();
+  rows::after_previous();
   const int col = blockIdx.x * 32 + threadIdx.x % 32, w = threadIdx.x / 32;
   float s = 0.f;
   if (col < H2)
@@ -1037,6 +1043,8 @@ struct Packing {
 // values themselves, rows padded with zeros to a multiple of 16 bytes.
 template <class T>
 __global__ void __launch_bounds__(256) k_pack(const Packing one, const Packing two) {
+  rows::let_next_start();
+  rows::after_previous();
   const int64_t n1 = one.rows * (one.cols_p / 8), n2 = two.rows * (two.cols_p / 8);
   for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n1 + n2;
        i += int64_t(gridDim.x) * 256) {
@@ -1177,8 +1185,7 @@ int launch_mode(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap&
       return SMC_ERR_CUDA;
     if (dev >= 0 && dev < kMaxDev) attr_set[dev] = true;
   }
-  kern<<<2 * a.pairs, kThreads, L::kBytes, s>>>(ma, mb, mo, md, a);
-  return cudaGetLastError() == cudaSuccess ? SMC_OK : SMC_ERR_CUDA;
+  return rows::launch_after(kern, dim3(2 * a.pairs), kThreads, L::kBytes, s, ma, mb, mo, md, a);
 }
 
 template <int MODE, int DT>
@@ -1223,8 +1230,8 @@ struct Run {
     const Packing pw{g.W, reinterpret_cast<uint16_t*>(work + lay.w),
                      lay.pack_w ? 2 * int64_t(g.cin) : 0, g.hidden, lay.Hp};
     const int64_t blocks = parts_up(px.rows * (px.cols_p / 8) + pw.rows * (pw.cols_p / 8), 256);
-    k_pack<T><<<unsigned(std::min<int64_t>(blocks, sm_pairs() * 32)), 256, 0, s>>>(px, pw);
-    return cudaGetLastError() == cudaSuccess ? SMC_OK : SMC_ERR_CUDA;
+    return rows::launch_after(k_pack<T>, dim3(unsigned(std::min<int64_t>(blocks, sm_pairs() * 32))),
+                              256, 0, s, px, pw);
   }
 
   // x [parts][n][Cp], W [parts][2][C][Hp], dgu [n][parts][2][Hp]
@@ -1302,17 +1309,16 @@ struct Run {
     auto join = (int64_t(tiles) * a.k_iters + 1) * a.pairs < (int64_t(1) << 32)
                     ? (few ? k_join_dw<T, uint32_t, 1> : k_join_dw<T, uint32_t, 4>)
                     : (few ? k_join_dw<T, uint64_t, 1> : k_join_dw<T, uint64_t, 4>);
-    join<<<dim3(tiles, few ? bn : bn / 4), 256, 0, s>>>(
-        a.slots, static_cast<T*>(dW), g.cin, g.hidden, a.m_tiles, a.n_tiles, a.k_iters, a.pairs, bn);
-    return cudaGetLastError() == cudaSuccess ? SMC_OK : SMC_ERR_CUDA;
+    return rows::launch_after(join, dim3(tiles, few ? bn : bn / 4), 256, 0, s, a.slots,
+                              static_cast<T*>(dW), g.cin, g.hidden, a.m_tiles, a.n_tiles, a.k_iters,
+                              a.pairs, bn);
   }
 
   int grad_bias(void* dbias) {
     const int H2 = 2 * g.hidden;
-    k_join_db<T><<<unsigned(parts_up(H2, 32)), 1024, 0, s>>>(
-        reinterpret_cast<const float*>(work + lay.db), static_cast<T*>(dbias),
-        parts_up(g.n, 32), H2);
-    return cudaGetLastError() == cudaSuccess ? SMC_OK : SMC_ERR_CUDA;
+    return rows::launch_after(k_join_db<T>, dim3(unsigned(parts_up(H2, 32))), 1024, 0, s,
+                              reinterpret_cast<const float*>(work + lay.db),
+                              static_cast<T*>(dbias), parts_up(g.n, 32), H2);
   }
 };
 

@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(32 * kRingWarps, ring_blocks(VECS * V))
 k_norm_bwd(const T* __restrict__ x, const float* __restrict__ gamma, const T* __restrict__ dy,
            T* __restrict__ dx, float* __restrict__ part, int64_t n, int c, int chunk_rows,
            int slot_bytes, float inv_c, float eps) {
+  rows::let_next_start();  // the join
   using S = Share<T, V, G, VECS, WHOLE>;
   constexpr int P = S::P, N = S::N, kRingStages = ring_stages(N);
   constexpr bool kKeep = N <= 20;  // dy * gamma stays in registers, else dy is read again
@@ -405,6 +406,7 @@ template <class T, int V, int G, int VECS>
 __global__ void __launch_bounds__(kThreads)
 k_norm_bwd_wide(const T* __restrict__ x, const float* __restrict__ gamma, const T* __restrict__ dy,
            T* __restrict__ dx, float* __restrict__ part, int64_t n, int c, float inv_c, float eps) {
+  rows::let_next_start();  // the join
   constexpr int kGroups = kThreads / G;
   __shared__ float smem[kThreads / 32];
   __shared__ float2 smem2[kThreads / 32];
@@ -569,6 +571,8 @@ __global__ void __launch_bounds__(1024)
 k_norm_join(const float* __restrict__ part, float* __restrict__ dgamma, float* __restrict__ dbeta,
             int64_t parts, int64_t c) {
   __shared__ float sums[32][33];
+  rows::let_next_start();
+  rows::after_previous();
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t col = blockIdx.x * int64_t(32) + lane;
   float s = 0.f;
@@ -826,7 +830,8 @@ int layer_norm_backward(const void* x, const float* gamma, const void* dy, void*
       if (rc != SMC_OK) return rc;
     }
     if (dgamma)
-      k_norm_join<<<unsigned((2 * c + 31) / 32), 1024, 0, s>>>(part, dgamma, dbeta, parts, c);
+      return rows::launch_after(k_norm_join, dim3(unsigned((2 * c + 31) / 32)), 1024, 0, s,
+                                static_cast<const float*>(part), dgamma, dbeta, parts, c);
     return launched();
   });
 }

@@ -65,6 +65,36 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// A kernel of a chain may be placed on the GPU while the one before it in the
+// stream runs out (launch_after): it sets itself up, and waits with
+// after_previous() before it touches memory that another kernel may use.
+// let_next_start() lets the next one of the chain be placed likewise.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... P, class... A>
+int launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                 A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(unsigned(threads));
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  if (cudaLaunchKernelEx(&c, kernel, P(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return SMC_ERR_CUDA;
+  }
+  return SMC_OK;
+}
+
 // f(T()) for the element type T of an smc_dtype.
 template <class F>
 int by_type(int dtype, F&& f) {
