@@ -499,8 +499,8 @@ int smc_gated_workspace(smc_handle_t h, int cin, int hidden, int dtype, int back
  *             adds state[1] to offset: a captured graph draws new masks at
  *             each replay when the caller advances state[1] between them.
  * Arithmetic is fp32, rounded once to dtype.  Asynchronous on stream.
- * Errors: SMC_ERR_INVALID (null or misaligned pointers, count < 0, bad dtype
- * or p, out overlapping an input in any other way), SMC_ERR_CUDA.
+ * Errors: SMC_ERR_INVALID (null or misaligned pointers, count < 0 or >= 2^42,
+ * bad dtype or p, out overlapping an input in any other way), SMC_ERR_CUDA.
  */
 int smc_dropout(const void* x, const void* residual, void* out, int64_t count, int dtype, double p,
                 uint64_t seed, uint64_t offset, const uint64_t* state, smc_stream_t stream);

@@ -529,7 +529,7 @@ int smc_gated_backward(smc_handle_t h, const void* feats, const void* W, const v
 int smc_dropout(const void* x, const void* residual, void* out, int64_t count, int dtype, double p,
                 uint64_t seed, uint64_t offset, const uint64_t* state, smc_stream_t stream) {
   if (count < 0 || elem_bytes(dtype) == 0 || !(p >= 0.0 && p <= 1.0)) return SMC_ERR_INVALID;
-  if (count >= (int64_t(1) << 44)) return SMC_ERR_INVALID;
+  if (count >= (int64_t(1) << 42)) return SMC_ERR_INVALID;  // 2^31 blocks of the kernel
   if (!aligned16(state)) return SMC_ERR_INVALID;
   if (count == 0) return SMC_OK;
   if (!x || !out || !aligned16(x) || !aligned16(out) || !aligned16(residual))

@@ -138,14 +138,15 @@ def act(name, v):
 class Gated:
     """The gated product and its gradients in float64, with their bounds."""
 
-    def __init__(self, x, W, bias, activation, dh=None):
+    def __init__(self, x, W, bias, activation, dh=None, terms=lambda m: 2 * (m + 2)):
+        """terms(m): how many roundings of 2^-24 a sum of m products may carry."""
         self.dtype, self.act = x.dtype, activation
         x, W = x.double(), W.double()
         b = torch.zeros(2, W.shape[2], dtype=torch.float64, device=x.device) if bias is None else \
             bias.double()
         g, u = x @ W[0] + b[0], x @ W[1] + b[1]
         c = x.shape[1]
-        acc = (c + 2) * 2 * E32
+        acc = terms(c) * E32
         dg, du = (acc * (x.abs() @ W[k].abs() + b[k].abs()) for k in (0, 1))
         a, s = act(activation, g)
         ev = 2.0 ** -20 * (1 + g.abs())  # of the activation or its slope
@@ -167,14 +168,14 @@ class Gated:
         self.dx = G @ W[0].T + U @ W[1].T
         self.dx_bound = rounding(self.dx, self.dtype) + 1.01 * (
             eg @ W[0].abs().T + eu @ W[1].abs().T +
-            (2 * h + 2) * 2 * E32 * (G.abs() @ W[0].abs().T + U.abs() @ W[1].abs().T))
+            terms(2 * h) * E32 * (G.abs() @ W[0].abs().T + U.abs() @ W[1].abs().T))
         xa = x.abs().T
         self.dW = torch.stack([x.T @ G, x.T @ U])
         self.dW_bound = rounding(self.dW, self.dtype) + 1.01 * torch.stack(
-            [xa @ e + (n + 2) * 2 * E32 * (xa @ v.abs()) for e, v in ((eg, G), (eu, U))])
+            [xa @ e + terms(n) * E32 * (xa @ v.abs()) for e, v in ((eg, G), (eu, U))])
         self.db = torch.stack([G.sum(0), U.sum(0)])
         self.db_bound = rounding(self.db, self.dtype) + 1.01 * torch.stack(
-            [e.sum(0) + (n + 2) * 2 * E32 * v.abs().sum(0) for e, v in ((eg, G), (eu, U))])
+            [e.sum(0) + terms(n) * E32 * v.abs().sum(0) for e, v in ((eg, G), (eu, U))])
 
 
 # ---------------------------------------------------------------------------

@@ -211,6 +211,70 @@ def test_gated_many_rows(dt):
         assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+def test_gated_fp32_long_sums():
+    """fp32 sums are accumulated 64 terms at a time (24 steps of the matrix unit,
+    each cutting up to two roundings, and 4 for the parts that are dropped) and
+    added up with one rounding per 64 terms and per share of the rows (at most
+    148); the bias gradient adds 32 rows by 5 steps, then the 32-row sums."""
+    for n, c, h in ((64, 4096, 72), (20001, 100, 136), (300, 64, 3000)):
+        with _index(n) as idx:
+            x, W, b, dh = _gated_inputs(n, c, h, "f32", seed=110)
+            ref = rc.Gated(x, W, b, "silu", dh, terms=lambda m: 52 + m // 64 + 148)
+            dx, dW, db = idx.gated_backward(x, W, dh, b)
+            rc.assert_close(idx.gated_forward(x, W, b), ref.out, ref.out_bound, f"{n} {c} {h} out")
+            rc.assert_close(dx, ref.dx, ref.dx_bound, f"{n} {c} {h} grad_in")
+            rc.assert_close(dW, ref.dW, ref.dW_bound, f"{n} {c} {h} grad_W")
+            rc.assert_close(db, ref.db, ref.db_bound, f"{n} {c} {h} grad_bias")
+
+
+_ABORT_SCRIPT = r"""
+import sys, torch
+sys.path.insert(0, {root!r})
+from submanifold_sparse_convolution_coord_b200.binding import SubMIndex
+statuses = []
+for n, c, h, dt in [(20000, 128, 512, torch.float16), (3000, 64, 64, torch.bfloat16),
+                    (3000, 100, 130, torch.float32)]:
+    i = torch.arange(n, device="cuda")
+    idx = SubMIndex(torch.stack([i * 0, i // 4096, i // 64 % 64, i % 64], 1).to(torch.int32))
+    x = torch.randn(n, c, device="cuda").to(dt)
+    W = torch.randn(2, c, h, device="cuda").to(dt)
+    b, dh = torch.randn(2, h, device="cuda").to(dt), torch.randn(n, h, device="cuda").to(dt)
+    for _ in range(2):
+        idx.gated_forward(x, W, b)
+        idx.gated_backward(x, W, dh, b)
+    torch.cuda.synchronize()
+    statuses.append(idx.status())
+    idx.close()
+print("statuses", statuses)
+"""
+
+
+@pytest.mark.parametrize("limit_ns,must_abort", [(200, True), (20000, False)])
+def test_gated_bounded_wait_abort_path(limit_ns, must_abort):
+    """With the wait limit cut to a debug value, waits give up in mid-pipeline:
+    the kernels drain what they issued, free tensor memory, return and report
+    through the status word, and the context stays usable."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = _ABORT_SCRIPT.format(root=os.path.dirname(here))
+    env = dict(os.environ, SMC_DEBUG_WAIT_LIMIT_NS=str(limit_ns))
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    line = [ln for ln in r.stdout.splitlines() if ln.startswith("statuses")][0]
+    statuses = eval(line.split(" ", 1)[1])
+    assert all(s in (0, -8) for s in statuses), statuses  # ok or a timeout, nothing else
+    if must_abort:
+        # a wait that the hardware's own suspension covers never looks at the
+        # limit, as in short chains of stages; the first case has long ones
+        assert statuses[0] == -8, statuses
+    with _index(700) as idx:  # the normal limit, in this process
+        x, W, b, dh = _gated_inputs(700, 128, 256, "f16", seed=120)
+        _check_gated(idx, x, W, b, "silu", dh, "after abort runs")
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 def test_gated_large_pre_activations(dt):
     """Gates far out on both sides: the activation's tails."""
