@@ -137,6 +137,11 @@ def _dev_ptr(t: torch.Tensor, name: str, dtype=None) -> int:
     return t.data_ptr()
 
 
+# the current stream's pointer, without the stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _Call:
     """The device and stream of one row-operator call.  Inside `with _Call(x,
     stream) as c`, x's device is current and tensors are allocated on the call's
@@ -160,7 +165,7 @@ class _Call:
             self._contexts = (torch.cuda.device(index),)
         for c in self._contexts:
             c.__enter__()
-        self.stream = torch.cuda.current_stream(index).cuda_stream
+        self.stream = _raw_stream(index)
         return self
 
     def __exit__(self, *exc):

@@ -50,7 +50,8 @@ constexpr int kBK = 64;  // depth of a stage: one 128-byte row of 16-bit values
 // Sixteen epilogue warps, four per quarter of the tensor-memory lanes: a warp's
 // way through a chunk is a chain of latencies (accumulator load, exponential,
 // division, staging, fence), so each scheduler gets four of them to interleave
-// (55,100 rows, 512 -> 2048 bf16, SiLU: TODO us with eight, TODO us with sixteen).
+// (55,100 rows, 512 -> 2048 bf16, SiLU: 201 us with eight, 180 us with
+// sixteen; its backward's first product 325 and 287 us).
 constexpr int kEpiWarp0 = 4, kEpiWarps = 16;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kSmemMax = 227 * 1024;
@@ -65,7 +66,7 @@ constexpr uint64_t kAbortDrainNs = 50000000ull;
 // The products of parts that are accumulated, smallest first.  A
 // stage holds all three parts of its A and B, so that 96 KB of loads feed six
 // products (with a stage per product it would be 192 KB: 26,214 rows, 128 -> 512:
-// 36.7 us, TODO us so).
+// 36.7 us, 31.5 us so).
 constexpr int kPartPairs = 6;
 __host__ __device__ constexpr int part_a(int q) { return q == 0 ? 2 : (q == 2 || q == 3 ? 1 : 0); }
 __host__ __device__ constexpr int part_b(int q) { return q == 1 ? 2 : (q == 2 || q == 4 ? 1 : 0); }
@@ -257,9 +258,11 @@ struct Smem {
   static constexpr int kChunks = (kTileChunks + 3) / 4;  // per warp
   // kPreBwd: dh of this tile (dg takes its place) and of the next, and du;
   // fp32, whose tiles take six times the products, reads dh and writes the
-  // parts of dg and du directly.  kPre, kDx: the outgoing chunk.  kDw stores
-  // from registers.
-  static constexpr int kSlots = MODE == kDw ? 0 : (MODE == kPreBwd ? (DT == SMC_F32 ? 0 : 3) : 1);
+  // parts of dg and du directly.  kPre, kDx: two outgoing chunks in turn (fp32:
+  // one).  kDw stores from registers.
+  static constexpr int kSlots = MODE == kDw       ? 0
+                                : MODE == kPreBwd ? (DT == SMC_F32 ? 0 : 3)
+                                                  : (DT == SMC_F32 ? 1 : 2);
   static constexpr int kWarpStage = kSlots * kChunkBytes;
   static constexpr int kBias = 128;  // bias of a warp's chunk: of g, then of u
   static constexpr int kTailBytes = kEpiWarps * kBias + 512;  // and the barriers
@@ -716,7 +719,7 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
     const uint32_t dh_bar0 = dh0 + 16 * w;
     const int hc = group * 32;  // kPre, kPreBwd: the warp's chunk of every tile
     const int64_t my_rows = rank * 128 + quarter * 32;
-    int seg = 0;
+    int seg = 0, stored = 0;  // stored: the slot of the next store
     uint32_t dh_phases = 0;  // the parity to wait for next, per slot
     bool ok = *abort_flag == 0;
 
@@ -828,7 +831,8 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
           if (!kStageSums) release();
           continue;
         }
-        uint8_t* out = mine;  // kPre: act(g) u; kPreBwd: dh, then dg
+        // kPre: act(g) u, in the slot of the store before last; kPreBwd: dh, then dg
+        uint8_t* out = mine + (MODE == kPre && DT != SMC_F32 ? stored * L::kChunkBytes : 0);
         if constexpr (MODE == kPreBwd && DT != SMC_F32) {
           out += slot * L::kChunkBytes;
           if (a.tma_dh) {
@@ -838,7 +842,8 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
           }
           if (lane == 0) bulk_wait_read<0>();  // du of the last tile
         } else {
-          if (lane == 0) bulk_wait_read<0>();  // the last tile's store has left the staging
+          if (lane == 0) bulk_wait_read<MODE == kPre && DT != SMC_F32 ? 1 : 0>();
+          stored ^= 1;
         }
         __syncwarp();
         uint8_t* out_u = mine + 2 * L::kChunkBytes;  // kPreBwd, 16-bit
@@ -920,7 +925,9 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
 #pragma unroll
             for (int part = 0; part < 32 / L::kCols; ++part) {
               if (col + part * L::kCols >= a.C) continue;
-              if (lane == 0) bulk_wait_read<0>();
+              uint8_t* to = mine + (DT != SMC_F32 ? stored * L::kChunkBytes : 0);
+              stored ^= 1;
+              if (lane == 0) bulk_wait_read<DT != SMC_F32 ? 1 : 0>();
               __syncwarp();
 #pragma unroll
               for (int g8 = 0; g8 < L::kCols / 8; ++g8) {
@@ -929,9 +936,9 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                   f[i] = make_float2(__uint_as_float(from[2 * i]), __uint_as_float(from[2 * i + 1]));
-                put8<DT>(mine, lane, g8, f);
+                put8<DT>(to, lane, g8, f);
               }
-              store_chunk<DT>(&map_out, a.tma_out, mine, a.out, row0, col + part * L::kCols, a.n,
+              store_chunk<DT>(&map_out, a.tma_out, to, a.out, row0, col + part * L::kCols, a.n,
                               a.C, lane);
             }
           } else {
@@ -973,31 +980,61 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   }
 }
 
-// dW of the tiles that several pairs worked on: their partial tiles in the
-// order of the pairs.  A block takes COLS columns (input channels) of a tile; a
-// thread has up to eight pairs' values of each in flight.  I: an integer that
-// holds the tiles times their stages times the pairs (32 bits divide several
-// times faster).
+// The joins behind the products: dW of the tiles that several pairs worked on
+// (their partial tiles in the order of the pairs), and dbias (the sums over 32
+// rows in a fixed order).  One launch: blocks of dbias first.
+struct JoinArgs {
+  const float* slots;
+  void* dW;  // null: no dW blocks
+  int C, H, m_tiles, n_tiles, k_iters, pairs, bn;
+  const float* db_part;
+  void* dbias;  // null: no dbias blocks
+  int64_t db_blocks;  // sums per column
+  int db_grid;        // blocks of dbias
+};
+
+// A block takes COLS columns (input channels) of a tile; a thread has up to
+// eight pairs' values of each in flight.  I: an integer that holds the tiles
+// times their stages times the pairs (32 bits divide several times faster).
 template <class T, class I, int COLS>
-__global__ void __launch_bounds__(256)
-k_join_dw(const float* __restrict__ slots, T* __restrict__ dW, int C, int H, int m_tiles,
-          int n_tiles, int k_iters, int pairs, int bn) {
+__global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
   rows::let_next_start();
   rows::after_previous();
-  int tile = blockIdx.x;
-  const int cl = blockIdx.y * COLS, c = tile / (2 * m_tiles) * bn + cl;
-  if (c >= C) return;
-  const I all = I(2) * m_tiles * n_tiles * k_iters;
-  const I i0 = I(tile) * k_iters, i1 = i0 + k_iters;
-  const int p0 = int(((i0 + 1) * pairs - 1) / all), p1 = int((i1 * pairs - 1) / all);
+  int block = blockIdx.x;
+  if (block < a.db_grid) {
+    // 32 columns; eight warps take every eighth sum, then the warps in order
+    __shared__ float sums[8][33];
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32, H2 = 2 * a.H;
+    const int col = block * 32 + lane;
+    float s = 0.f;
+    if (col < H2) {
+#pragma unroll 8
+      for (int64_t b = w; b < a.db_blocks; b += 8) s += a.db_part[b * H2 + col];
+    }
+    sums[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && col < H2) {
+      for (int i = 1; i < 8; ++i) s += sums[i][lane];
+      static_cast<T*>(a.dbias)[col] = rows::from_float<T>(s);
+    }
+    return;
+  }
+  block -= a.db_grid;
+  const int per_tile = a.bn / COLS;
+  int tile = block / per_tile;
+  const int cl = block % per_tile * COLS, c = tile / (2 * a.m_tiles) * a.bn + cl;
+  if (c >= a.C) return;
+  const I all = I(2) * a.m_tiles * a.n_tiles * a.k_iters;
+  const I i0 = I(tile) * a.k_iters, i1 = i0 + a.k_iters;
+  const int p0 = int(((i0 + 1) * a.pairs - 1) / all), p1 = int((i1 * a.pairs - 1) / all);
   if (p0 == p1) return;  // one pair stored it whole
   // the first pair used its second slot if the tile starts its last segment
-  const int64_t first = 2 * p0 + (p0 * all / pairs > i0 ? 0 : 1);
-  tile %= 2 * m_tiles;
-  const int64_t s = tile / m_tiles, h = int64_t(tile % m_tiles) * 256 + threadIdx.x;
-  if (h >= H) return;
-  const float* from = slots + cl * 256 + threadIdx.x;
-  const int64_t slot = int64_t(bn) * 256;
+  const int64_t first = 2 * int64_t(p0) + (p0 * all / a.pairs > i0 ? 0 : 1);
+  tile %= 2 * a.m_tiles;
+  const int64_t s = tile / a.m_tiles, h = int64_t(tile % a.m_tiles) * 256 + threadIdx.x;
+  if (h >= a.H) return;
+  const float* from = a.slots + cl * 256 + threadIdx.x;
+  const int64_t slot = int64_t(a.bn) * 256;
   float v[COLS];
 #pragma unroll
   for (int i = 0; i < COLS; ++i) v[i] = from[first * slot + i * 256];
@@ -1006,29 +1043,10 @@ k_join_dw(const float* __restrict__ slots, T* __restrict__ dW, int C, int H, int
 #pragma unroll
     for (int i = 0; i < COLS; ++i) v[i] += from[2 * p * slot + i * 256];
   }
+  T* to = static_cast<T*>(a.dW) + (s * a.C + c) * a.H + h;
 #pragma unroll
   for (int i = 0; i < COLS; ++i)
-    if (c + i < C) dW[(s * C + c + i) * H + h] = rows::from_float<T>(v[i]);
-}
-
-// dbias: the sums over 32 rows, added up in a fixed order.
-template <class T>
-__global__ void __launch_bounds__(1024)
-k_join_db(const float* __restrict__ part, T* __restrict__ dbias, int64_t blocks, int H2) {
-  __shared__ float sums[32][33];
-  rows::let_next_start();
-  rows::after_previous();
-  const int col = blockIdx.x * 32 + threadIdx.x % 32, w = threadIdx.x / 32;
-  float s = 0.f;
-  if (col < H2)
-#pragma unroll 8
-    for (int64_t b = w; b < blocks; b += 32) s += part[b * H2 + col];
-  sums[w][threadIdx.x % 32] = s;
-  __syncthreads();
-  if (w == 0 && col < H2) {
-    for (int i = 1; i < 32; ++i) s += sums[i][threadIdx.x];
-    dbias[col] = rows::from_float<T>(s);
-  }
+    if (c + i < a.C) to[int64_t(i) * a.H] = rows::from_float<T>(v[i]);
 }
 
 // A matrix [rows][cols] and its 16-bit copy [parts][rows][cols_p].
@@ -1296,29 +1314,51 @@ struct Run {
     a.m_tiles = int(parts_up(g.hidden, 256));
     a.n_tiles = int(parts_up(g.cin, bn));
     a.k_iters = int(parts_up(g.n, kBK));
-    const int tiles = 2 * a.m_tiles * a.n_tiles;
-    a.pairs = int(std::min<int64_t>(sm_pairs(), int64_t(tiles) * a.k_iters));
+    a.pairs = int(std::min<int64_t>(sm_pairs(), int64_t(2) * a.m_tiles * a.n_tiles * a.k_iters));
     a.out = dW;
     a.slots = reinterpret_cast<float*>(work + lay.slots);
     if (!map_dgu(&ma, kBK, kBK) || !map_x(&mb, kBK, kBK)) return SMC_ERR_CUDA;
-    const int rc = launch_bn<kDw, DT>(bn, ma, mb, mo, md, a, s);
-    if (rc != SMC_OK) return rc;
-    // one column per block while the blocks are few (two tiles of 37 parts each:
-    // 5 us, with four 14.5), else four (32 tiles: 12 us, with one 28)
-    const bool few = int64_t(tiles) * bn < 4096;
-    auto join = (int64_t(tiles) * a.k_iters + 1) * a.pairs < (int64_t(1) << 32)
-                    ? (few ? k_join_dw<T, uint32_t, 1> : k_join_dw<T, uint32_t, 4>)
-                    : (few ? k_join_dw<T, uint64_t, 1> : k_join_dw<T, uint64_t, 4>);
-    return rows::launch_after(join, dim3(tiles, few ? bn : bn / 4), 256, 0, s, a.slots,
-                              static_cast<T*>(dW), g.cin, g.hidden, a.m_tiles, a.n_tiles, a.k_iters,
-                              a.pairs, bn);
+    return launch_bn<kDw, DT>(bn, ma, mb, mo, md, a, s);
   }
 
-  int grad_bias(void* dbias) {
-    const int H2 = 2 * g.hidden;
-    return rows::launch_after(k_join_db<T>, dim3(unsigned(parts_up(H2, 32))), 1024, 0, s,
-                              reinterpret_cast<const float*>(work + lay.db),
-                              static_cast<T*>(dbias), parts_up(g.n, 32), H2);
+  // What is left of grad_w (its arguments are still in `a`) and of the bias.
+  int join(void* dW, void* dbias) {
+    JoinArgs j = {};
+    int64_t blocks = 0;
+    bool few = true, small = true;
+    if (dW) {
+      const int tiles = 2 * a.m_tiles * a.n_tiles;
+      const int64_t all = int64_t(tiles) * a.k_iters;
+      bool split = false;  // a pair's share ends inside a tile
+      for (int64_t p = 1; p < a.pairs; ++p) split |= p * all / a.pairs % a.k_iters != 0;
+      if (split) {
+        j.slots = a.slots;
+        j.dW = dW;
+        j.C = a.C;
+        j.m_tiles = a.m_tiles;
+        j.n_tiles = a.n_tiles;
+        j.k_iters = a.k_iters;
+        j.pairs = a.pairs;
+        j.bn = Layout::bn_for(g.cin);
+        // one column per block while the blocks are few (two tiles of 37 parts
+        // each: 5 us, with four 14.5), else four (32 tiles: 11 us, with one 28)
+        few = int64_t(tiles) * j.bn < 4096;
+        small = (all + 1) * a.pairs < (int64_t(1) << 32);
+        blocks = int64_t(tiles) * (few ? j.bn : j.bn / 4);
+      }
+    }
+    j.H = g.hidden;
+    if (dbias) {
+      j.db_part = reinterpret_cast<const float*>(work + lay.db);
+      j.dbias = dbias;
+      j.db_blocks = parts_up(g.n, 32);
+      j.db_grid = int(parts_up(2 * g.hidden, 32));
+      blocks += j.db_grid;
+    }
+    if (blocks == 0) return SMC_OK;
+    auto kern = small ? (few ? k_join<T, uint32_t, 1> : k_join<T, uint32_t, 4>)
+                      : (few ? k_join<T, uint64_t, 1> : k_join<T, uint64_t, 4>);
+    return rows::launch_after(kern, dim3(unsigned(blocks)), 256, 0, s, j);
   }
 };
 
@@ -1357,7 +1397,7 @@ int gated_backward(const GatedCall& g, const void* dh, void* dx, void* dW, void*
     if (rc == SMC_OK) rc = r.pre(nullptr, dh, dbias != nullptr);
     if (rc == SMC_OK && dx) rc = r.grad_x(dx);
     if (rc == SMC_OK && dW) rc = r.grad_w(dW);
-    if (rc == SMC_OK && dbias) rc = r.grad_bias(dbias);
+    if (rc == SMC_OK && (dW || dbias)) rc = r.join(dW, dbias);
     return rc;
   });
 }
