@@ -830,7 +830,7 @@ int layer_norm_backward(const void* x, const float* gamma, const void* dy, void*
       if (rc != SMC_OK) return rc;
     }
     if (dgamma)
-      return rows::launch_after(k_norm_join, dim3(unsigned((2 * c + 31) / 32)), 1024, 0, s,
+      return rows::launch_after(true, k_norm_join, dim3(unsigned((2 * c + 31) / 32)), 1024, 0, s,
                                 static_cast<const float*>(part), dgamma, dbeta, parts, c);
     return launched();
   });

@@ -75,19 +75,20 @@ __device__ __forceinline__ void after_previous() {
 __device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// early = false: an ordinary launch.
 template <class... P, class... A>
-int launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                 A... args) {
+int launch_after(bool early, void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                 cudaStream_t s, A... args) {
   cudaLaunchConfig_t c = {};
   c.gridDim = grid;
   c.blockDim = dim3(unsigned(threads));
   c.dynamicSmemBytes = smem;
   c.stream = s;
-  cudaLaunchAttribute early = {};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &early;
-  c.numAttrs = 1;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &attr;
+  c.numAttrs = early ? 1 : 0;
   if (cudaLaunchKernelEx(&c, kernel, P(args)...) != cudaSuccess) {
     cudaGetLastError();
     return SMC_ERR_CUDA;
