@@ -117,6 +117,63 @@ __device__ __forceinline__ float2 share_stats(const RowShare<T, V, G, VECS>& x, 
   return make_float2(mean, rsqrtf(group_sum<G>(s, smem) * inv_c + eps));
 }
 
+// A thread's share of a row as pairs: value k is vector k / V, element k % V.
+// WHOLE: the row fills every thread's share.
+template <class T, int V, int G, int VECS, bool WHOLE>
+struct Share {
+  static constexpr int N = VECS * V, P = (N + 1) / 2;
+  // column of value k
+  static __device__ __forceinline__ int column(int lane, int k) {
+    return (lane + k / V * G) * V + k % V;
+  }
+  static __device__ __forceinline__ void raw(const T* row, int lane, int c, bool ok,
+                                             Vec<T, V> (&q)[VECS]) {
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int at = (lane + i * G) * V;
+      q[i] = Vec<T, V>{};
+      if (ok && (WHOLE || at < c)) q[i] = *reinterpret_cast<const Vec<T, V>*>(row + at);
+    }
+  }
+  static __device__ __forceinline__ void expand(const Vec<T, V> (&q)[VECS], float2 (&v)[P]) {
+    float f[2 * P];
+    f[2 * P - 1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[i * V + j] = rows::to_float(q[i].v[j]);
+#pragma unroll
+    for (int p = 0; p < P; ++p) v[p] = make_float2(f[2 * p], f[2 * p + 1]);
+  }
+  static __device__ __forceinline__ void load(const T* row, int lane, int c, float2 (&v)[P]) {
+    Vec<T, V> q[VECS];
+    raw(row, lane, c, true, q);
+    expand(q, v);
+  }
+  // Takes the mean from the values (columns outside the row stay 0) and gives
+  // the sum of their squares.
+  static __device__ __forceinline__ float centre(float2 (&v)[P], float mean, int lane, int c) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float2 m = make_float2(-mean, -mean);
+      if constexpr (!WHOLE || N % 2 != 0) {
+        if (2 * p + 1 >= N || column(lane, 2 * p + 1) >= c) m.y = 0.f;
+        if (column(lane, 2 * p) >= c) m.x = 0.f;
+      }
+      v[p] = add2(v[p], m);
+      s = fma2(v[p], v[p], s);
+    }
+    return s.x + s.y;
+  }
+  static __device__ __forceinline__ float sum(const float2 (&v)[P]) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < P; ++p) s = add2(s, v[p]);
+    return s.x + s.y;
+  }
+};
+
 // V consecutive floats (16-byte aligned when V is a multiple of 4).
 template <int V>
 __device__ __forceinline__ void load_floats(const float* p, float (&v)[V]) {
@@ -146,11 +203,13 @@ constexpr int norm_threads() {
   return G <= 32 ? 128 : kThreads;
 }
 
-template <class T, int V, int G, int VECS>
-__global__ void __launch_bounds__(norm_threads<G>(), G > 32 ? 1 : (VECS == 1 ? 8 : (VECS * V <= 16 ? 4 : 2)))
+template <class T, int V, int G, int VECS, bool WHOLE>
+__global__ void __launch_bounds__(norm_threads<G>(),
+                                  G > 32 ? 1 : (VECS == 1 ? 8 : (VECS * V <= 16 ? 4 : 2)))
 k_norm(const T* x, const float* __restrict__ gamma, const float* __restrict__ beta, T* out,
        int64_t n, int c, float inv_c, float eps) {
-  constexpr int R = rows_per_group<T, V, VECS>();
+  using S = Share<T, V, G, VECS, WHOLE>;
+  constexpr int R = rows_per_group<T, V, VECS>(), P = S::P;
   constexpr int kGroups = norm_threads<G>() / G;
   __shared__ float smem[kThreads / 32];
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
@@ -158,44 +217,60 @@ k_norm(const T* x, const float* __restrict__ gamma, const float* __restrict__ be
   const int rows_here = int(min(n - base, int64_t(kGroups * R)));
   x += base * c;
   out += base * c;
-  RowShare<T, V, G, VECS> share[R];
+  Vec<T, V> raw[R][VECS];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     const int r = group + k * kGroups;
-    share[k].load(x + int64_t(r) * c, lane, c, r < rows_here);
+    S::raw(x + int64_t(r) * c, lane, c, r < rows_here, raw[k]);
   }
   // one vector a thread: gamma and beta in registers for all R rows
   constexpr bool kHold = VECS == 1;
   float gm[kHold ? VECS : 1][V], bt[kHold ? VECS : 1][V];
   if constexpr (kHold) {
-#pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-      const int at = (lane + i * G) * V;
-      if (gamma && at < c) load_floats(gamma + at, gm[i]);
-      if (beta && at < c) load_floats(beta + at, bt[i]);
-    }
+    if (gamma && (WHOLE || lane * V < c)) load_floats(gamma + lane * V, gm[0]);
+    if (beta && (WHOLE || lane * V < c)) load_floats(beta + lane * V, bt[0]);
   }
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     const int r = group + k * kGroups;
-    const float2 st = share_stats(share[k], lane, c, inv_c, eps, smem);
+    float2 v[P];
+    S::expand(raw[k], v);
+    const float mean = group_sum<G>(S::sum(v), smem) * inv_c;
+    const float squares = S::centre(v, mean, lane, c);
+    const float rstd = rsqrtf(group_sum<G>(squares, smem) * inv_c + eps);
     if (r >= rows_here) continue;
+    float y[2 * P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const float2 q = mul2(v[p], make_float2(rstd, rstd));
+      y[2 * p] = q.x;
+      y[2 * p + 1] = q.y;
+    }
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
       const int at = (lane + i * G) * V, h = kHold ? i : 0;
-      if (at >= c) continue;
+      if (!WHOLE && at >= c) continue;
       if constexpr (!kHold) {
         if (gamma) load_floats(gamma + at, gm[0]);
         if (beta) load_floats(beta + at, bt[0]);
       }
+      float* z = y + i * V;
+      if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+          float2 q = make_float2(z[j], z[j + 1]);
+          if (gamma) q = mul2(q, make_float2(gm[h][j], gm[h][j + 1]));
+          if (beta) q = add2(q, make_float2(bt[h][j], bt[h][j + 1]));
+          z[j] = q.x;
+          z[j + 1] = q.y;
+        }
+      } else {
+        if (gamma) z[0] *= gm[h][0];
+        if (beta) z[0] += bt[h][0];
+      }
       Vec<T, V> o;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float v = (share[k].value(i, j) - st.x) * st.y;
-        if (gamma) v *= gm[h][j];
-        if (beta) v += bt[h][j];
-        o.v[j] = rows::from_float<T>(v);
-      }
+      for (int j = 0; j < V; ++j) o.v[j] = rows::from_float<T>(z[j]);
       *reinterpret_cast<Vec<T, V>*>(out + int64_t(r) * c + at) = o;
     }
   }
@@ -204,36 +279,6 @@ k_norm(const T* x, const float* __restrict__ gamma, const float* __restrict__ be
 // ---------------------------------------------------------------------------
 // backward, rows of up to a warp
 // ---------------------------------------------------------------------------
-// A lane's share of a row as pairs: value k is vector k / V, element k % V.
-template <class T, int V, int G, int VECS, bool WHOLE>
-struct Share {
-  static constexpr int N = VECS * V, P = (N + 1) / 2;
-  // column of value k
-  static __device__ __forceinline__ int column(int lane, int k) {
-    return (lane + k / V * G) * V + k % V;
-  }
-  // From a row in shared memory; zeros outside it (WHOLE: there is no outside).
-  static __device__ __forceinline__ void load(const T* row, int lane, int c, float2 (&v)[P]) {
-    float f[2 * P];
-    f[2 * P - 1] = 0.f;
-#pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-      const int at = (lane + i * G) * V;
-      Vec<T, V> q;
-      if constexpr (WHOLE) {
-        q = *reinterpret_cast<const Vec<T, V>*>(row + at);
-      } else {
-        q = Vec<T, V>{};
-        if (at < c) q = *reinterpret_cast<const Vec<T, V>*>(row + at);
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) f[i * V + j] = rows::to_float(q.v[j]);
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p) v[p] = make_float2(f[2 * p], f[2 * p + 1]);
-  }
-};
-
 constexpr int kRingWarps = 8;
 // Two blocks per SM with three slots a warp, or, where a lane's share of a row
 // is more than 16 values (registers for one block), one with four.
@@ -312,22 +357,9 @@ k_norm_bwd(const T* __restrict__ x, const float* __restrict__ gamma, const T* __
       const bool ok = r < n;
       float2 xc[P], g[P];
       S::load(xs + row * c, lane, c, xc);
-      float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int p = 0; p < P; ++p) s = add2(s, xc[p]);
-      const float mean = group_sum<G>(s.x + s.y, nullptr) * inv_c;
-      s = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        float2 m = make_float2(-mean, -mean);
-        if constexpr (!WHOLE || N % 2 != 0) {  // columns outside the row stay 0
-          if (2 * p + 1 >= N || S::column(lane, 2 * p + 1) >= c) m.y = 0.f;
-          if (S::column(lane, 2 * p) >= c) m.x = 0.f;
-        }
-        xc[p] = add2(xc[p], m);
-        s = fma2(xc[p], xc[p], s);
-      }
-      float rstd = rsqrtf(group_sum<G>(s.x + s.y, nullptr) * inv_c + eps);
+      const float mean = group_sum<G>(S::sum(xc), nullptr) * inv_c;
+      const float squares = S::centre(xc, mean, lane, c);
+      float rstd = rsqrtf(group_sum<G>(squares, nullptr) * inv_c + eps);
       if (!ok) rstd = 0.f;  // a row that does not exist: eps = 0 made it infinite
       const float2 rr = make_float2(rstd, rstd);
       float2 s1 = make_float2(0.f, 0.f), s2 = s1;
@@ -760,7 +792,11 @@ int layer_norm(const void* x, const float* gamma, const float* beta, void* out, 
     return by_deal<T, false>(d, [&](auto v, auto g, auto vecs) {
       constexpr int V = decltype(v)::value, G = decltype(g)::value, K = decltype(vecs)::value;
       const int64_t step = norm_threads<G>() / G * rows_per_group<T, V, K>();
-      k_norm<T, V, G, K><<<unsigned((n + step - 1) / step), norm_threads<G>(), 0, s>>>(
+      // rows that fill every thread's share are the common ones: no masks
+      auto kern = k_norm<T, V, G, K, false>;
+      if constexpr (V * sizeof(T) >= 8)
+        if (c == G * K * V) kern = k_norm<T, V, G, K, true>;
+      kern<<<unsigned((n + step - 1) / step), norm_threads<G>(), 0, s>>>(
           in, gamma, beta, o, n, int(c), 1.f / float(c), eps);
       return launched();
     });

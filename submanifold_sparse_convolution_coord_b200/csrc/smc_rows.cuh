@@ -65,6 +65,20 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// Two floats rounded to a word of two 16-bit values.
+template <class T>
+__device__ __forceinline__ uint32_t pack2_of(float2 v);
+template <>
+__device__ __forceinline__ uint32_t pack2_of<__half>(float2 v) {
+  const __half2 h = __float22half2_rn(v);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2_of<__nv_bfloat16>(float2 v) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(v);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // A kernel of a chain may be placed on the GPU while the one before it in the
 // stream runs out (launch_after): it sets itself up, and waits with
 // after_previous() before it touches memory that another kernel may use.
