@@ -981,61 +981,31 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   }
 }
 
-// The joins behind the products: dW of the tiles that several pairs worked on
-// (their partial tiles in the order of the pairs), and dbias (the sums over 32
-// rows in a fixed order).  One launch: blocks of dbias first.
-struct JoinArgs {
-  const float* slots;
-  void* dW;  // null: no dW blocks
-  int C, H, m_tiles, n_tiles, k_iters, pairs, bn;
-  const float* db_part;
-  void* dbias;  // null: no dbias blocks
-  int64_t db_blocks;  // sums per column
-  int db_grid;        // blocks of dbias
-};
-
-// A block takes COLS columns (input channels) of a tile; a thread has up to
-// eight pairs' values of each in flight.  I: an integer that holds the tiles
-// times their stages times the pairs (32 bits divide several times faster).
+// dW of the tiles that several pairs worked on: their partial tiles in the
+// order of the pairs.  A block takes COLS columns (input channels) of a tile; a
+// thread has up to eight pairs' values of each in flight.  I: an integer that
+// holds the tiles times their stages times the pairs (32 bits divide several
+// times faster).
 template <class T, class I, int COLS>
-__global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
+__global__ void __launch_bounds__(256)
+k_join_dw(const float* __restrict__ slots, T* __restrict__ dW, int C, int H, int m_tiles,
+          int n_tiles, int k_iters, int pairs, int bn) {
   rows::let_next_start();
   rows::after_previous();
-  int block = blockIdx.x;
-  if (block < a.db_grid) {
-    // 32 columns; eight warps take every eighth sum, then the warps in order
-    __shared__ float sums[8][33];
-    const int lane = threadIdx.x % 32, w = threadIdx.x / 32, H2 = 2 * a.H;
-    const int col = block * 32 + lane;
-    float s = 0.f;
-    if (col < H2) {
-#pragma unroll 8
-      for (int64_t b = w; b < a.db_blocks; b += 8) s += a.db_part[b * H2 + col];
-    }
-    sums[w][lane] = s;
-    __syncthreads();
-    if (w == 0 && col < H2) {
-      for (int i = 1; i < 8; ++i) s += sums[i][lane];
-      static_cast<T*>(a.dbias)[col] = rows::from_float<T>(s);
-    }
-    return;
-  }
-  block -= a.db_grid;
-  const int per_tile = a.bn / COLS;
-  int tile = block / per_tile;
-  const int cl = block % per_tile * COLS, c = tile / (2 * a.m_tiles) * a.bn + cl;
-  if (c >= a.C) return;
-  const I all = I(2) * a.m_tiles * a.n_tiles * a.k_iters;
-  const I i0 = I(tile) * a.k_iters, i1 = i0 + a.k_iters;
-  const int p0 = int(((i0 + 1) * a.pairs - 1) / all), p1 = int((i1 * a.pairs - 1) / all);
+  int tile = blockIdx.x;
+  const int cl = blockIdx.y * COLS, c = tile / (2 * m_tiles) * bn + cl;
+  if (c >= C) return;
+  const I all = I(2) * m_tiles * n_tiles * k_iters;
+  const I i0 = I(tile) * k_iters, i1 = i0 + k_iters;
+  const int p0 = int(((i0 + 1) * pairs - 1) / all), p1 = int((i1 * pairs - 1) / all);
   if (p0 == p1) return;  // one pair stored it whole
   // the first pair used its second slot if the tile starts its last segment
-  const int64_t first = 2 * int64_t(p0) + (p0 * all / a.pairs > i0 ? 0 : 1);
-  tile %= 2 * a.m_tiles;
-  const int64_t s = tile / a.m_tiles, h = int64_t(tile % a.m_tiles) * 256 + threadIdx.x;
-  if (h >= a.H) return;
-  const float* from = a.slots + cl * 256 + threadIdx.x;
-  const int64_t slot = int64_t(a.bn) * 256;
+  const int64_t first = 2 * int64_t(p0) + (p0 * all / pairs > i0 ? 0 : 1);
+  tile %= 2 * m_tiles;
+  const int64_t s = tile / m_tiles, h = int64_t(tile % m_tiles) * 256 + threadIdx.x;
+  if (h >= H) return;
+  const float* from = slots + cl * 256 + threadIdx.x;
+  const int64_t slot = int64_t(bn) * 256;
   float v[COLS];
 #pragma unroll
   for (int i = 0; i < COLS; ++i) v[i] = from[first * slot + i * 256];
@@ -1044,10 +1014,31 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
 #pragma unroll
     for (int i = 0; i < COLS; ++i) v[i] += from[2 * p * slot + i * 256];
   }
-  T* to = static_cast<T*>(a.dW) + (s * a.C + c) * a.H + h;
 #pragma unroll
   for (int i = 0; i < COLS; ++i)
-    if (c + i < a.C) to[int64_t(i) * a.H] = rows::from_float<T>(v[i]);
+    if (c + i < C) dW[(s * C + c + i) * H + h] = rows::from_float<T>(v[i]);
+}
+
+// dbias: the sums over 32 rows, added up in a fixed order: a block takes 32
+// columns, its 32 warps every 32nd sum, then the warps in order.
+template <class T>
+__global__ void __launch_bounds__(1024)
+k_join_db(const float* __restrict__ part, T* __restrict__ dbias, int64_t blocks, int H2) {
+  __shared__ float sums[32][33];
+  rows::let_next_start();
+  rows::after_previous();
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32, col = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (col < H2) {
+#pragma unroll 8
+    for (int64_t b = w; b < blocks; b += 32) s += part[b * H2 + col];
+  }
+  sums[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && col < H2) {
+    for (int i = 1; i < 32; ++i) s += sums[i][lane];
+    dbias[col] = rows::from_float<T>(s);
+  }
 }
 
 // A matrix [rows][cols] and its 16-bit copy [parts][rows][cols_p].
@@ -1279,11 +1270,19 @@ struct Run {
                      64 / kE, 32, 1);
   }
 
+  // 256 columns a tile, or 128 where there are no more columns, or so few rows
+  // that 256 would leave half of the SMs without a tile: a tile of 128 takes half
+  // the time.  (11 rows, 896 -> 1600: bf16 forward 8.6 -> 7.3 us and
+  // backward 35 -> 31, fp32 34 -> 23 and 141 -> 91; from 2,000 rows on both alike.)
+  static int tile_columns(int m_tiles, int64_t columns) {
+    return columns > 128 && 2 * m_tiles * parts_up(columns, 256) > sm_pairs() ? 256 : 128;
+  }
+
   // out = act(g) u, or (dh given) dg and du into the workspace
   int pre(void* out, const void* dh, bool want_db) {
     CUtensorMap ma, mb, mo = {}, md = {};
-    const int bn = g.hidden > 64 ? 256 : 128;
     a.m_tiles = int(parts_up(g.n, 256));
+    const int bn = tile_columns(a.m_tiles, 2 * int64_t(g.hidden));
     a.n_tiles = int(parts_up(g.hidden, bn / 2));
     a.k_iters = int(parts_up(g.cin, kBK));
     a.pairs = int(std::min<int64_t>(sm_pairs(), int64_t(a.m_tiles) * a.n_tiles));
@@ -1302,8 +1301,8 @@ struct Run {
 
   int grad_x(void* dx) {
     CUtensorMap ma, mb, mo = {}, md = {};
-    const int bn = Layout::bn_for(g.cin);
     a.m_tiles = int(parts_up(g.n, 256));
+    const int bn = tile_columns(a.m_tiles, g.cin);
     a.n_tiles = int(parts_up(g.cin, bn));
     a.k_iters = 2 * int(parts_up(g.hidden, kBK));
     a.pairs = int(std::min<int64_t>(sm_pairs(), int64_t(a.m_tiles) * a.n_tiles));
@@ -1327,44 +1326,30 @@ struct Run {
     return launch_bn<kDw, DT>(bn, ma, mb, mo, md, a, s);
   }
 
-  // What is left of grad_w (its arguments are still in `a`) and of the bias.
+  // The joins behind grad_w (its arguments are still in `a`) and pre.
   int join(void* dW, void* dbias) {
-    JoinArgs j = {};
-    int64_t blocks = 0;
-    bool few = true, small = true;
     if (dW) {
-      const int tiles = 2 * a.m_tiles * a.n_tiles;
+      const int tiles = 2 * a.m_tiles * a.n_tiles, bn = Layout::bn_for(g.cin);
       const int64_t all = int64_t(tiles) * a.k_iters;
       bool split = false;  // a pair's share ends inside a tile
       for (int64_t p = 1; p < a.pairs; ++p) split |= p * all / a.pairs % a.k_iters != 0;
       if (split) {
-        j.slots = a.slots;
-        j.dW = dW;
-        j.C = a.C;
-        j.m_tiles = a.m_tiles;
-        j.n_tiles = a.n_tiles;
-        j.k_iters = a.k_iters;
-        j.pairs = a.pairs;
-        j.bn = Layout::bn_for(g.cin);
         // one column per block while the blocks are few (two tiles of 37 parts
         // each: 5 us, with four 14.5), else four (32 tiles: 11 us, with one 28)
-        few = int64_t(tiles) * j.bn < 4096;
-        small = (all + 1) * a.pairs < (int64_t(1) << 32);
-        blocks = int64_t(tiles) * (few ? j.bn : j.bn / 4);
+        const bool few = int64_t(tiles) * bn < 4096, small = (all + 1) * a.pairs < int64_t(1) << 32;
+        auto kern = small ? (few ? k_join_dw<T, uint32_t, 1> : k_join_dw<T, uint32_t, 4>)
+                          : (few ? k_join_dw<T, uint64_t, 1> : k_join_dw<T, uint64_t, 4>);
+        const int rc = rows::launch_after(
+            a.early, kern, dim3(tiles, few ? bn : bn / 4), 256, 0, s, a.slots, static_cast<T*>(dW),
+            g.cin, g.hidden, a.m_tiles, a.n_tiles, a.k_iters, a.pairs, bn);
+        if (rc != SMC_OK) return rc;
       }
     }
-    j.H = g.hidden;
-    if (dbias) {
-      j.db_part = reinterpret_cast<const float*>(work + lay.db);
-      j.dbias = dbias;
-      j.db_blocks = parts_up(g.n, 32);
-      j.db_grid = int(parts_up(2 * g.hidden, 32));
-      blocks += j.db_grid;
-    }
-    if (blocks == 0) return SMC_OK;
-    auto kern = small ? (few ? k_join<T, uint32_t, 1> : k_join<T, uint32_t, 4>)
-                      : (few ? k_join<T, uint64_t, 1> : k_join<T, uint64_t, 4>);
-    return rows::launch_after(a.early, kern, dim3(unsigned(blocks)), 256, 0, s, j);
+    if (!dbias) return SMC_OK;
+    const int H2 = 2 * g.hidden;
+    return rows::launch_after(a.early, k_join_db<T>, dim3(unsigned(parts_up(H2, 32))), 1024, 0, s,
+                              reinterpret_cast<const float*>(work + lay.db),
+                              static_cast<T*>(dbias), parts_up(g.n, 32), H2);
   }
 };
 
