@@ -427,7 +427,10 @@ int smc_layer_norm_backward_workspace(int64_t n, int64_t c, int dtype, int64_t* 
  *          may be NULL when that is 0), not shared with a call that may run
  *          at the same time; it needs no initialisation.
  * Products are accumulated in fp32; bias, activation and product are applied
- * to the accumulators and the result is rounded once to dtype.
+ * to the accumulators and the result is rounded once to dtype.  SMC_F32 values
+ * are multiplied as the sum of three bf16 parts, which is exact to 2^-24 of each
+ * product; an infinite value among them gives NaN in its row, and values below
+ * 2^-110 lose their last bits.
  * Asynchronous on stream, never synchronises; calls on one handle may run on
  * different streams at once (each with its own workspace).
  * Errors: as smc_forward; SMC_ERR_INVALID also for a bad activation, a

@@ -134,6 +134,34 @@ def test_norm_gradient_against_differences():
         assert abs(diff - float(sum(terms))) <= 1e-5 * size
 
 
+def test_norm_far_rows():
+    """More than 2^31 elements: rows at the start, around 2^31 elements and at
+    the end equal those of a call on these rows alone."""
+    n, c = 33_600_000, 64
+    x = torch.empty(n, c, dtype=torch.bfloat16, device=DEV)
+    picked = [slice(0, 300), slice((1 << 31) // c - 150, (1 << 31) // c + 150), slice(n - 300, n)]
+    x.fill_(1.0)
+    for k, rows in enumerate(picked):
+        x[rows] = _randn(300, c, seed=60 + k, dtype=torch.bfloat16)
+    _, gamma, beta, _ = _norm_inputs(2, c, torch.bfloat16, seed=63)
+    y = smc_layer_norm(x, gamma, beta)
+    for rows in picked:
+        assert torch.equal(y[rows], smc_layer_norm(x[rows].clone(), gamma, beta))
+    # y has served; its memory takes the gradient
+    dx, dgamma, dbeta = smc_layer_norm_backward(x, gamma, x, grad_in=y)
+    for rows in picked:
+        part = x[rows].clone()
+        assert torch.equal(dx[rows], smc_layer_norm_backward(part, gamma, part)[0])
+    # the constant rows have xhat = 0 (their mean is exact) and add n - 900 to dbeta
+    parts = [rc.norm_grads(x[rows], gamma, x[rows], 1e-5) for rows in picked]
+    want = sum(p[2] for p in parts) + (n - 900)
+    size = sum(x[rows].double().abs().sum(0) for rows in picked) + (n - 900)
+    rc.assert_close(dbeta, want, n * rc.E32 * size, "dbeta")
+    want = sum(p[1] for p in parts)
+    bound = sum(rc.norm_grads_bound(x[rows], gamma, x[rows], 1e-5, x.dtype)[1] for rows in picked)
+    rc.assert_close(dgamma, want, bound + 1000 * rc.E32 * 900, "dgamma")
+
+
 def test_norm_refusals():
     x, gamma, beta, dy = _norm_inputs(8, 64, torch.float16, seed=23)
     with pytest.raises(ValueError):
@@ -323,6 +351,66 @@ def test_gated_gradient_against_differences():
                     loss(*(v - s * e for v, e in zip(at, d)))) / (2 * s)
             size = sum(float((a * e).abs().sum()) for a, e in zip(grads, d))
             assert abs(diff - sum(float((a * e).sum()) for a, e in zip(grads, d))) <= 1e-5 * size
+
+
+def test_gated_far_rows():
+    """More than 2^31 hidden values: rows at the start, around 2^31 values and at
+    the end, and the weight gradient of all rows (added up in float64 in pieces)."""
+    n, c, h = 1_100_000, 16, 2048
+    with _index(n) as idx:
+        x, W, b, dh = _gated_inputs(n, c, h, "bf16", seed=130)
+        out = idx.gated_forward(x, W, b)
+        dx, dW, db = idx.gated_backward(x, W, dh, b)
+        at = (1 << 31) // h
+        for rows in (slice(0, 200), slice(at - 100, at + 100), slice(n - 200, n)):
+            ref = rc.Gated(x[rows], W, b, "silu", dh[rows])
+            rc.assert_close(out[rows], ref.out, ref.out_bound, "out")
+            rc.assert_close(dx[rows], ref.dx, ref.dx_bound, "grad_in")
+        want = bound = 0
+        for r in range(0, n, 100_000):
+            ref = rc.Gated(x[r:r + 100_000], W, b, "silu", dh[r:r + 100_000], terms=lambda m: 0)
+            want = want + ref.dW
+            bound = bound + ref.dW_bound
+            del ref
+        # each piece's bound holds a rounding of its own, and no accumulation error:
+        # that of n rows, in shares of n / 37, is far below the roundings of dg and du
+        assert (dW.double() - want).norm() <= bound.norm()
+        assert idx.status() == 0
+
+
+def test_gated_first_call_captured():
+    """The first call of a process may be one that a graph captures."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from submanifold_sparse_convolution_coord_b200.binding import (SubMIndex, smc_dropout, smc_layer_norm,
+                                                               smc_layer_norm_backward)
+i = torch.arange(500, device="cuda")
+idx = SubMIndex(torch.stack([i * 0, i * 0, i // 64, i % 64], 1).to(torch.int32))
+x = torch.randn(500, 100, device="cuda").half()
+W, dh = torch.randn(2, 100, 64, device="cuda").half(), torch.randn(500, 64, device="cuda").half()
+gamma = torch.ones(100, device="cuda")
+def step():
+    y = smc_layer_norm(x, gamma)
+    out = smc_dropout(idx.gated_forward(y, W), 0.1, 3)
+    dx, dW, _ = idx.gated_backward(y, W, dh)
+    return (out, dW) + smc_layer_norm_backward(x, gamma, dx)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    captured = step()
+g.replay()
+torch.cuda.synchronize()
+eager = step()
+assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+assert idx.status() == 0
+print("same")
+""".format(root=here)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
 
 
 def test_gated_wanted_gradients_only_and_rows_behind():
@@ -579,3 +667,12 @@ def test_explicit_stream():
         assert torch.equal(got, want) and torch.equal(dx, wdx) and torch.equal(dg, wdg)
         assert torch.equal(db, wdb) and torch.equal(d, drop)
         del trash
+    with _index(3000) as idx:
+        x, W, b, dh = _gated_inputs(3000, 100, 192, "f32", seed=140)
+        want = (idx.gated_forward(x, W, b),) + idx.gated_backward(x, W, dh, b)
+        got = [torch.empty_like(v) for v in want]
+        s.wait_stream(torch.cuda.current_stream())
+        binding.smc_gated_forward(idx.handle, x, W, got[0], 100, 192, b, stream=s)
+        binding.smc_gated_backward(idx.handle, x, W, dh, *got[1:], 100, 192, b, stream=s)
+        s.synchronize()
+        assert all(torch.equal(a, v) for a, v in zip(got, want))
