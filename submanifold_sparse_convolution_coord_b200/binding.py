@@ -185,7 +185,12 @@ def _operand(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape,
     `like`'s dtype unless another is given; None for None."""
     if t is None:
         return None
-    ptr = _dev_ptr(t, name, like.dtype if dtype is None else dtype)
+    if dtype is None:
+        dtype = like.dtype
+    if t.dtype == dtype and t.shape == shape and t.is_cuda and t.is_contiguous() and \
+            t.get_device() == like.get_device():
+        return t.data_ptr()
+    ptr = _dev_ptr(t, name, dtype)  # says what is wrong, if it is one of its checks
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.device != like.device:
@@ -403,9 +408,10 @@ def smc_layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
     gp = _operand(gamma, "gamma", x, (c,), torch.float32)
     bp = _operand(beta, "beta", x, (c,), torch.float32)
     with _Call(x, stream) as call:
+        op = _operand(out, "out", x, x.shape)
         if out is None:
             out = torch.empty_like(x)
-        op = _operand(out, "out", x, (n, c))
+            op = out.data_ptr()
         _check(lib().smc_layer_norm(xp, gp, bp, op, n, c, code, float(eps), call.stream),
                "smc_layer_norm")
         call.keep(x, gamma, beta, out)
@@ -431,9 +437,10 @@ def smc_layer_norm_backward(x: torch.Tensor, gamma: Optional[torch.Tensor],
     gp = _operand(gamma, "gamma", x, (c,), torch.float32)
     yp = _operand(grad_out, "grad_out", x, (n, c))
     with _Call(x, stream) as call:
+        ip = _operand(grad_in, "grad_in", x, x.shape)
         if grad_in is None:
             grad_in = torch.empty_like(x)
-        ip = _operand(grad_in, "grad_in", x, (n, c))
+            ip = grad_in.data_ptr()
         dgamma = dbeta = None
         if gamma is not None:
             dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
@@ -534,9 +541,10 @@ def smc_dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
     rp = _operand(residual, "residual", x, x.shape)
     sp = _operand(state, "state", x, (2,), torch.int64)
     with _Call(x, stream) as call:
+        op = _operand(out, "out", x, x.shape)
         if out is None:
             out = torch.empty_like(x)
-        op = _operand(out, "out", x, x.shape)
+            op = out.data_ptr()
         _check(lib().smc_dropout(xp, rp, op, x.numel(), DTYPE_CODE[x.dtype], float(p), seed, offset,
                                  sp, call.stream), "smc_dropout")
         call.keep(x, residual, state, out)
