@@ -363,7 +363,8 @@ int smc_forward_ex(smc_handle_t h, const void* feats, const void* W, void* out, 
  * eps         : >= 0, added to the variance.
  * Statistics and arithmetic are fp32; the result is rounded once to dtype.
  * A row's result depends on that row alone (an infinite or NaN value makes
- * its own row NaN and no other).  Asynchronous on stream; no workspace.
+ * its own row NaN and no other; a row whose squared deviations pass the range
+ * of fp32 gives beta).  Asynchronous on stream; no workspace.
  * Errors: SMC_ERR_INVALID (null or misaligned pointers, bad sizes, dtype or
  * eps, out overlapping an input in any other way), SMC_ERR_UNSUPPORTED (n or
  * c >= 2^31), SMC_ERR_CUDA.

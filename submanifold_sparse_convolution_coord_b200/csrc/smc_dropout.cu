@@ -67,7 +67,8 @@ __device__ __forceinline__ float2 pair_of(const Group<T>& g, int j) {
 constexpr int kThreads = 256;
 template <class T, bool RES, bool STATE>
 __global__ void __launch_bounds__(kThreads, 2048 / kThreads)
-k_dropout(const T* x, const T* residual, T* out, int64_t count, const __grid_constant__ DropArgs a) {
+k_dropout(const T* x, const T* residual, T* out, int64_t count,
+          const __grid_constant__ DropArgs a) {
   const int64_t g = blockIdx.x * int64_t(kThreads) + threadIdx.x;
   if (g * 8 >= count) return;
   const bool whole = g * 8 + 8 <= count;
