@@ -293,7 +293,7 @@ constexpr int ring_stages(int values) { return values > 16 ? 4 : 3; }
 // 16-byte accesses.  A lane keeps the sums of dgamma and dbeta for
 // its columns, which are the same in every row; the block joins them at the
 // end: part[block][2][c].  (209,715 x 128 fp16: 37 us with loads to registers,
-// 33 us so.)
+// 33 us with chunks of 2 KB, 31 us with 1 KB.)
 template <class T, int V, int G, int VECS, bool WHOLE>
 __global__ void __launch_bounds__(32 * kRingWarps, ring_blocks(VECS * V))
 k_norm_bwd(const T* __restrict__ x, const float* __restrict__ gamma, const T* __restrict__ dy,
@@ -752,10 +752,13 @@ int by_deal(const Deal& d, F&& f) {
   }
 }
 
-// Launch of the backward kernels.  Ring (groups of up to a warp): chunks of
-// up to 2 KB, whole passes of a warp; one or two blocks per SM.  Wide groups: a
-// few blocks per SM.  Each block leaves one partial sum, and there are no more
-// blocks than work.
+// Launch of the backward kernels.  Ring (groups of up to a warp): chunks of the
+// fewest whole passes of a warp that hold 1 KB, one or two blocks per SM.  (The
+// most passes within 2 KB: 209,715 x 128 fp16 37.6 us, 34.2 so, 200,000 x 96 the
+// same 39.6; within 1 KB, one pass where that is 600 to 800 bytes: 96 channels
+// 41.5; more slots of 1 KB, 128 channels 37.4 with four, 39 with six.)  Wide
+// groups: a few blocks per SM.  Each block leaves one partial sum, and there are
+// no more blocks than work.
 struct BwdPlan {
   Deal d;
   int chunk_rows = 0, slot_bytes = 0, smem = 0;
@@ -769,7 +772,7 @@ struct BwdPlan {
       return;
     }
     const int pass = 32 / d.g;
-    chunk_rows = pass * int(std::max<int64_t>(1, 2048 / (pass * c * elem)));
+    chunk_rows = pass * int((1024 + pass * c * elem - 1) / (pass * c * elem));
     slot_bytes = int((chunk_rows * c * elem + 15 + 15) / 16 * 16);
     const int values = d.vecs * d.v;
     smem = std::max(kRingWarps * ring_stages(values) * 2 * slot_bytes, kRingWarps * 2 * int(c) * 4);
