@@ -427,8 +427,10 @@ int smc_layer_norm_backward_workspace(int64_t n, int64_t c, int dtype, int64_t* 
  * workspace   : device pointer to smc_gated_workspace bytes (16-byte aligned;
  *          may be NULL when that is 0), not shared with a call that may run
  *          at the same time; it needs no initialisation.
- * Products are accumulated in fp32; bias, activation and product are applied
- * to the accumulators and the result is rounded once to dtype.  SMC_F32 values
+ * Products are accumulated in fp32 (the matrix unit cuts its sums, so they are
+ * taken in pieces of at most 4096 terms, 64 for SMC_F32, that are added up with
+ * rounding); bias, activation and product are applied to the accumulators and
+ * the result is rounded once to dtype.  SMC_F32 values
  * are multiplied as the sum of three bf16 parts, which is exact to 2^-24 of each
  * product; an infinite value among them gives NaN in its row, and values below
  * 2^-110 lose their last bits.

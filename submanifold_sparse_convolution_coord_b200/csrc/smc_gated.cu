@@ -57,13 +57,23 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kSmemMax = 227 * 1024;
 constexpr uint64_t kAbortDrainNs = 50000000ull;
 
-// fp32 inputs: an accumulation in tensor memory cuts what falls below the sum's
-// last bit instead of rounding it, so its error grows with the number of steps
-// (2.3e-8 of the sum per 16-deep step was measured); each stage is therefore
-// accumulated on its own (24 steps) and the epilogue's warps add the stages up
-// in registers, rounding.
-//
-// The products of parts that are accumulated, smallest first.  A
+// An accumulation in tensor memory cuts what falls below the sum's last bit
+// instead of rounding it, so its error has one sign and grows with the number of
+// steps (terms of one sign lose 6.8e-8 of the final sum per 16-deep step: 8.5e-4
+// of a 16-bit dW over 200,000 rows, more than fp16's half step).  Long sums are
+// therefore accumulated in pieces, which the epilogue's warps add up in
+// registers, rounding: fp32 stage by stage (24 steps); 16-bit sums of more than 64
+// stages (LONG) 64 at a time (256 steps, 1.7e-5 of a piece).  Shorter ones go
+// without: the registers that the pieces take cost them time (26,214 rows 64 ->
+// 256, backward: 45.1 us with pieces throughout, 40.6 us so; 55,100 rows 512 ->
+// 2048, whose dW is long: 751 us, 750 us before there were pieces).
+constexpr int kLongStages = 64;
+template <int DT, bool LONG>
+constexpr int piece_stages() {  // 0: the whole range
+  return DT == SMC_F32 ? 1 : (LONG ? kLongStages : 0);
+}
+
+// fp32: the products of parts that are accumulated, smallest first.  A
 // stage holds all three parts of its A and B, so that 96 KB of loads feed six
 // products (with a stage per product it would be 192 KB: 26,214 rows, 128 -> 512:
 // 36.7 us, 31.5 us so).
@@ -551,7 +561,7 @@ __device__ __forceinline__ void gate16(const uint32_t (&gv)[16], const uint32_t 
     choose(std::false_type());
 }
 
-template <int MODE, int BN, int DT>
+template <int MODE, int BN, int DT, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
         const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_dh,
@@ -561,7 +571,8 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   constexpr int kStages = L::kStages;
   constexpr bool kPreMode = MODE == kPre || MODE == kPreBwd;
   constexpr uint32_t kTmemCols = 2 * BN;
-  constexpr bool kStageSums = DT == SMC_F32;
+  constexpr int kPiece = piece_stages<DT, LONG>();
+  constexpr bool kStageSums = kPiece > 0;  // pieces are added up in registers
   constexpr int kSums = kStageSums ? (kPreMode ? 2 : L::kChunks) * 32 : 1;
   // M = 256 over the pair; A is MN-major in kDw, B in all modes but kDx
   constexpr uint32_t kIdesc = (1u << 4) | ((DT != SMC_F16 ? 1u : 0u) << 7) |
@@ -672,7 +683,8 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
     while (ok && walk.next(g)) {
       int acc = 0;
       for (int it = g.k0; it < g.k1; ++it) {
-        if (kStageSums || it == g.k0) {  // a new accumulation
+        const int piece_it = kPiece > 0 ? (it - g.k0) % kPiece : it - g.k0;
+        if (piece_it == 0) {  // a new accumulation
           acc = seg & 1;
           if (!(ok = waits.wait(tempty0 + 8 * acc, ((seg >> 1) & 1) ^ 1))) break;
           ++seg;
@@ -691,11 +703,11 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
             const uint64_t db = MODE != kDx ? desc_b_mnmajor(sb + k * 2048, 8192)
                                             : desc_a_kmajor(sb + k * 32);
             umma_f16_pair(tmem + acc * BN, da, db, kIdesc,
-                          (!kStageSums && it > g.k0) || q > 0 || k > 0);
+                          piece_it > 0 || q > 0 || k > 0);
           }
         }
         umma_commit_pair(empty0 + 8 * st);
-        if (kStageSums || it + 1 == g.k1) umma_commit_pair(tfull0 + 8 * acc);
+        if (piece_it + 1 == kPiece || it + 1 == g.k1) umma_commit_pair(tfull0 + 8 * acc);
         if (++st == kStages) {
           st = 0;
           phase ^= 1;
@@ -792,12 +804,12 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
       };
-      // fp32: the stages' sums, added up.  Value i is column column_of(i / 32) + i % 32.
+      // The pieces' sums, added up.  Value i is column column_of(i / 32) + i % 32.
       float sums[kSums];
-      auto add_stages = [&](bool live, auto column_of) {
+      auto add_pieces = [&](bool live, auto column_of) {
 #pragma unroll
         for (int i = 0; i < kSums; ++i) sums[i] = 0.f;
-        for (int it = g.k0; it < g.k1; ++it) {
+        for (int it = g.k0; it < g.k1; it += kStageSums ? kPiece : 1) {
           if (!next_sums()) return false;
           if (live) {
 #pragma unroll
@@ -826,7 +838,7 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
         more = walk.next(gn);
         if (more) prefetch(gn, slot ^ 1);
         if constexpr (kStageSums) {
-          ok = add_stages(live, [&](int k) { return k * (BN / 2) + hc; });
+          ok = add_pieces(live, [&](int k) { return k * (BN / 2) + hc; });
           if (!ok) break;
         } else {
           if (!(ok = next_sums())) break;
@@ -908,7 +920,7 @@ k_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
       } else {
         more = walk.next(gn);
         if constexpr (kStageSums)
-          ok = add_stages(true, [&](int k) { return (group * L::kChunks + k) * 32; });
+          ok = add_pieces(true, [&](int k) { return (group * L::kChunks + k) * 32; });
         else
           ok = next_sums();
         if (!ok) break;
@@ -1183,12 +1195,12 @@ struct Layout {
   static int bn_for(int C) { return C > 128 ? 256 : 128; }
 };
 
-template <int MODE, int BN, int DT>
+template <int MODE, int BN, int DT, bool LONG>
 int launch_mode(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
                 const CUtensorMap& md, const GemmArgs& a, cudaStream_t s) {
   using L = Smem<MODE, BN, DT>;
   static_assert(L::kBytes <= kSmemMax, "shared memory");
-  auto kern = k_gated<MODE, BN, DT>;
+  auto kern = k_gated<MODE, BN, DT, LONG>;
   constexpr int kMaxDev = 64;
   static bool attr_set[kMaxDev] = {};
   int dev = -1;
@@ -1206,8 +1218,17 @@ int launch_mode(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap&
 template <int MODE, int DT>
 int launch_bn(int bn, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
               const CUtensorMap& md, const GemmArgs& a, cudaStream_t s) {
-  return bn == 256 ? launch_mode<MODE, 256, DT>(ma, mb, mo, md, a, s)
-                   : launch_mode<MODE, 128, DT>(ma, mb, mo, md, a, s);
+  if constexpr (DT != SMC_F32) {
+    // the longest accumulation: a tile's stages, or a pair's share of all of them
+    int64_t most = a.k_iters;
+    if (MODE == kDw)
+      most = std::min(most, parts_up(int64_t(2) * a.m_tiles * a.n_tiles * a.k_iters, a.pairs));
+    if (most > kLongStages)
+      return bn == 256 ? launch_mode<MODE, 256, DT, true>(ma, mb, mo, md, a, s)
+                       : launch_mode<MODE, 128, DT, true>(ma, mb, mo, md, a, s);
+  }
+  return bn == 256 ? launch_mode<MODE, 256, DT, false>(ma, mb, mo, md, a, s)
+                   : launch_mode<MODE, 128, DT, false>(ma, mb, mo, md, a, s);
 }
 
 template <int DT>

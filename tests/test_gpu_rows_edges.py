@@ -1,0 +1,121 @@
+"""Row operators on the GPU where rounding, range or sheer size could spoil them:
+sums of one sign over many rows, the tails of the activations, NaN and overflow,
+rows of extreme spread, and sums over many rows whose results are exact."""
+import pytest
+import torch
+
+from submanifold_sparse_convolution_coord_b200 import binding
+from submanifold_sparse_convolution_coord_b200.binding import (SubMIndex, smc_layer_norm,
+                                                               smc_layer_norm_backward)
+
+import rows_common as rc
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+def _rand(*shape, seed=0, lo=0.0, hi=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return lo + (hi - lo) * torch.rand(*shape, generator=g, device=DEV)
+
+
+def _randn(*shape, seed=0, dtype=torch.float32):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(*shape, generator=g, device=DEV).to(dtype)
+
+
+def _signs(*shape, seed=0, dtype=torch.float32):
+    """-1, 0 and 1."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randint(-1, 2, shape, generator=g, device=DEV, dtype=torch.int8).to(dtype)
+
+
+def _index(n):
+    i = torch.arange(n, device=DEV)
+    c = torch.stack([i // 2 ** 18, i // 4096 % 64, i // 64 % 64, i % 64], 1)
+    return SubMIndex(c.to(torch.int32))
+
+
+def _unit_gate(c, h, dtype):
+    """W and bias of a bilinear gate with both pre-activations 1: dg = du = dh."""
+    return torch.zeros(2, c, h, dtype=dtype, device=DEV), torch.ones(2, h, dtype=dtype, device=DEV)
+
+
+def _one_sign_allowance(pieces):
+    """A piece of a sum is 256 steps of the matrix unit, each cutting at most twice
+    2^-23 of a sum that grows evenly (half of its final size on average); the
+    pieces are added up with 2^-24 each.  Roundings of results to their type have
+    means of their own below 1e-6 (fp16) and 1e-5 (bf16)."""
+    return 256 * 2.0 ** -23 + pieces * rc.E32
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_gated_weight_gradient_of_one_sign(dt):
+    """All terms of the weight gradient positive, and enough tiles (80 for 74
+    pairs of SMs) that one accumulation takes all 200,000 rows.  The matrix unit
+    cuts its sums, so a loss has one sign and shows in the mean relative error."""
+    n, c, h, dtype = 200_000, 1024, 2368, rc.DTYPES[dt]
+    x = (_rand(n, c, seed=1, lo=0.5, hi=1.5) * _rand(c, seed=2, lo=1, hi=2)).to(dtype)
+    dh = (_rand(n, h, seed=3, lo=0.5, hi=1.5) * _rand(h, seed=4, lo=1, hi=2) / 16).to(dtype)
+    W, b = _unit_gate(c, h, dtype)
+    dW = torch.empty_like(W)
+    with _index(n) as idx:
+        binding.smc_gated_backward(idx.handle, x, W, dh, None, dW, None, c, h, b, "none")
+        assert idx.status() == 0
+    allowed = _one_sign_allowance(n / 4096)
+    xd = x.double().t()
+    for at in range(0, h, 592):
+        ref = xd @ dh[:, at:at + 592].double()
+        for half in range(2):
+            rel = dW[half, :, at:at + 592].double() / ref - 1
+            assert abs(float(rel.mean())) <= allowed + 1e-5, (half, at, float(rel.mean()))
+            assert float(rel.abs().max()) <= rc.UNIT[dtype] + 2 * allowed
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_gated_input_gradient_of_one_sign(dt):
+    """The same for the input gradient's sum over 2 x 65,536 hidden units.  x = 0
+    leaves both pre-activations at 1 whatever the weights."""
+    n, c, h, dtype = 300, 264, 65536, rc.DTYPES[dt]
+    x = torch.zeros(n, c, dtype=dtype, device=DEV)
+    W = (_rand(2, c, h, seed=1, lo=0.5, hi=1.5) * _rand(c, 1, seed=2, lo=1, hi=2) / 16).to(dtype)
+    dh = (_rand(n, h, seed=3, lo=0.5, hi=1.5) * _rand(n, 1, seed=4, lo=1, hi=2)).to(dtype)
+    b = torch.ones(2, h, dtype=dtype, device=DEV)
+    dx = torch.empty_like(x)
+    with _index(n) as idx:
+        binding.smc_gated_backward(idx.handle, x, W, dh, dx, None, None, c, h, b, "none")
+        assert idx.status() == 0
+    ref = dh.double() @ (W[0].double() + W[1].double()).t()
+    rel = dx.double() / ref - 1
+    allowed = _one_sign_allowance(2 * h / 4096)
+    assert abs(float(rel.mean())) <= allowed + 1e-5
+    assert float(rel.abs().max()) <= rc.UNIT[dtype] + 2 * allowed
+
+
+@pytest.mark.parametrize("n", [300, 60_000])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_gated_products_of_one_sign(dt, n):
+    """The same for the pre-activations' sums over 65,536 channels, and for dg and
+    du, which are computed from them again (up = 1, so out is the gate, du = dh g)."""
+    c, h, dtype = 65536 if n == 300 else 8200, 72, rc.DTYPES[dt]
+    x = (_rand(n, c, seed=1, lo=0.5, hi=1.5) * _rand(n, 1, seed=2, lo=1, hi=2)).to(dtype)
+    W = (_rand(2, c, h, seed=3, lo=0.5, hi=1.5) * _rand(h, seed=4, lo=1, hi=2) / 16).to(dtype)
+    W[1] = 0
+    b = torch.ones(2, h, dtype=dtype, device=DEV)
+    scale = 2.0 ** -7 if n == 300 else 2.0 ** -15  # the bias gradient stays in fp16's range
+    dh = torch.full((n, h), scale, dtype=dtype, device=DEV)
+    b[0] = 0
+    db = torch.empty_like(b)
+    with _index(n) as idx:
+        out = idx.gated_forward(x, W, b, "none")
+        binding.smc_gated_backward(idx.handle, x, W, dh, None, None, db, c, h, b, "none")
+        assert idx.status() == 0
+    ref = torch.cat([x[r:r + 5000].double() @ W[0].double() for r in range(0, n, 5000)])
+    rel = out.double() / ref - 1
+    allowed = _one_sign_allowance(c / 4096)
+    assert abs(float(rel.mean())) <= allowed + 1e-5
+    assert float(rel.abs().max()) <= rc.UNIT[dtype] + 2 * allowed
+    # the bias gradient: 32 rows by five steps, then at most 59 sums a warp, and 32 warps
+    rel = db[1].double() / (ref * scale).sum(0) - 1
+    assert float(rel.abs().max()) <= rc.UNIT[dtype] + 2 * allowed + 100 * rc.E32
