@@ -167,10 +167,11 @@ __device__ __forceinline__ float rcp_fast(float v) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 1 / (1 + exp(-v)); exp(-v) = inf gives the correct limit 0.
-__device__ __forceinline__ float2 sigmoid2(float2 v) {
+// 1 / (1 + e), e = exp(-v); e = inf gives the correct limit 0.
+__device__ __forceinline__ float2 sigmoid2(float2 v, float2& e) {
   const float2 x = mul2(v, dup2(-kLog2e));
-  const float2 d = add2(make_float2(exp2_fast(x.x), exp2_fast(x.y)), dup2(1.f));
+  e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+  const float2 d = add2(e, dup2(1.f));
   return make_float2(rcp_fast(d.x), rcp_fast(d.y));
 }
 
@@ -200,7 +201,10 @@ __device__ __forceinline__ float2 normal_cdf2(float2 v, float2& e) {
 template <int ACT>
 __device__ __forceinline__ float2 act_value2(float2 v) {
   if constexpr (ACT == SMC_ACT_RELU) return make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f));
-  if constexpr (ACT == SMC_ACT_SILU) return mul2(v, sigmoid2(v));
+  if constexpr (ACT == SMC_ACT_SILU) {
+    float2 e;
+    return mul2(v, sigmoid2(v, e));
+  }
   if constexpr (ACT == SMC_ACT_GELU) {
     float2 e;
     return mul2(v, normal_cdf2(v, e));
@@ -213,10 +217,13 @@ __device__ __forceinline__ void act_both2(float2 v, float2& value, float2& slope
     value = act_value2<ACT>(v);
     slope = make_float2(v.x > 0.f ? 1.f : 0.f, v.y > 0.f ? 1.f : 0.f);
   } else if constexpr (ACT == SMC_ACT_SILU) {
-    // s (1 + v (1 - s)) = s + a - a s, a = v s
-    const float2 s = sigmoid2(v);
+    // s + v s (1 - s) with 1 - s = e s: a difference of s and 1, or of v s and
+    // v s^2, would leave nothing of it for large v (s is 0 where e is infinite)
+    float2 e;
+    const float2 s = sigmoid2(v, e);
     value = mul2(v, s);
-    slope = fma2(mul2(value, s), dup2(-1.f), add2(s, value));
+    constexpr float kMax = 3.402823466e38f;
+    slope = fma2(value, mul2(make_float2(fminf(e.x, kMax), fminf(e.y, kMax)), s), s);
   } else if constexpr (ACT == SMC_ACT_GELU) {
     float2 e;
     const float2 c = normal_cdf2(v, e);

@@ -119,3 +119,36 @@ def test_gated_products_of_one_sign(dt, n):
     # the bias gradient: 32 rows by five steps, then at most 59 sums a warp, and 32 warps
     rel = db[1].double() / (ref * scale).sum(0) - 1
     assert float(rel.abs().max()) <= rc.UNIT[dtype] + 2 * allowed + 100 * rc.E32
+
+
+def _one_row(gate, dt, act):
+    """The gated product of one row whose pre-activations are `gate` and 1, and
+    the gradient by the gate for dh = 1: the activation's value and slope."""
+    dtype = rc.DTYPES[dt]
+    gate = torch.tensor(gate, dtype=torch.float64).to(dtype).to(DEV)
+    h = gate.numel()
+    x, W = torch.zeros(1, 8, dtype=dtype, device=DEV), torch.zeros(2, 8, h, dtype=dtype, device=DEV)
+    b, dh = torch.stack([gate, torch.ones_like(gate)]), torch.ones(1, h, dtype=dtype, device=DEV)
+    with _index(1) as idx:
+        out = idx.gated_forward(x, W, b, act)
+        _, _, db = idx.gated_backward(x, W, dh, b, act)
+    return gate.double().cpu(), out[0], db[0]
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_silu_far_out(dt):
+    """SiLU's slope is s + v s (1 - s) with 1 - s small for large v; both terms
+    carry some roundings of 2^-24, and an exponential of v < 0 the error of its
+    argument, |v| 2^-23.  Below -87 the kernel's exponential passes the range of
+    fp32 and the sigmoid is 0."""
+    big = [20, 50, 88, 100, 1e3, 3e4, 6e4]
+    if dt != "f16":
+        big += [1e5, 1e6, 3e7, 1e9, 1e20, 3e38]
+    gate = [s * v for v in big + [0, 0.5, 1, 2, 5, 10, 15] for s in (1, -1)]
+    v, out, slope = _one_row(gate, dt, "silu")
+    s, t = torch.sigmoid(v), torch.sigmoid(-v)
+    rel = (8 + 2 * (-v).clamp(0, 100)) * 2.0 ** -23
+    rc.assert_close(out, v * s, rc.rounding(v * s, out.dtype) + rel * (v * s).abs() + 1e-35, "value")
+    want = s + v * s * t
+    rc.assert_close(slope, want, rc.rounding(want, out.dtype) + rel * (s + v.abs() * s * t) + 1e-35,
+                    "slope")
