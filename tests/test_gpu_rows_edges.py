@@ -152,3 +152,18 @@ def test_silu_far_out(dt):
     want = s + v * s * t
     rc.assert_close(slope, want, rc.rounding(want, out.dtype) + rel * (s + v.abs() * s * t) + 1e-35,
                     "slope")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_gelu_tails(dt):
+    """GELU's value v cdf(v) and slope cdf(v) + v pdf(v), relative to the terms
+    themselves on both sides: 8 roundings of 2^-23 each around the exponential,
+    whose argument v^2 / 2 carries two roundings (v^2 2^-23 relative)."""
+    gate = [x / 16 for x in range(-12 * 16, 8 * 16 + 1)]
+    v, out, slope = _one_row(gate, dt, "gelu")
+    cdf = 0.5 * torch.erfc(-v / 2 ** 0.5)
+    pdf = torch.exp(-0.5 * v * v) / (2 * torch.pi) ** 0.5
+    rel = (8 + v * v) * 2.0 ** -23
+    rc.assert_close(out, v * cdf, rc.rounding(v * cdf, out.dtype) + rel * (v * cdf).abs(), "value")
+    want = cdf + v * pdf
+    rc.assert_close(slope, want, rc.rounding(want, out.dtype) + rel * (cdf + v.abs() * pdf), "slope")
