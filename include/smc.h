@@ -422,7 +422,7 @@ int smc_layer_norm_backward_workspace(int64_t n, int64_t c, int dtype, int64_t* 
  * bias   : device pointer, [2][hidden] of dtype, or NULL.
  * out    : device pointer, [n][hidden] of dtype; every element is overwritten.
  * activation : enum smc_activation, of the gate (SMC_ACT_NONE: a bilinear
- *          product).
+ *          product; a NaN gate stays NaN through every one of them).
  * cin, hidden : any value from 1 to 65536.
  * workspace   : device pointer to smc_gated_workspace bytes (16-byte aligned;
  *          may be NULL when that is 0), not shared with a call that may run

@@ -208,7 +208,8 @@ __device__ __forceinline__ float2 gelu2(float2 v, float2 a, float2 tail) {
 // products (see k_gated).
 template <int ACT>
 __device__ __forceinline__ float2 act_value2(float2 v) {
-  if constexpr (ACT == SMC_ACT_RELU) return make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f));
+  // a maximum with 0 would hide a NaN
+  if constexpr (ACT == SMC_ACT_RELU) return make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);
   if constexpr (ACT == SMC_ACT_SILU) {
     float2 e;
     return mul2(v, sigmoid2(v, e));
@@ -224,7 +225,7 @@ template <int ACT>
 __device__ __forceinline__ void act_both2(float2 v, float2& value, float2& slope) {
   if constexpr (ACT == SMC_ACT_RELU) {
     value = act_value2<ACT>(v);
-    slope = make_float2(v.x > 0.f ? 1.f : 0.f, v.y > 0.f ? 1.f : 0.f);
+    slope = make_float2(v.x > 0.f ? 1.f : value.x, v.y > 0.f ? 1.f : value.y);  // 0, or the NaN
   } else if constexpr (ACT == SMC_ACT_SILU) {
     // s + v s (1 - s) with 1 - s = e s: a difference of s and 1, or of v s and
     // v s^2, would leave nothing of it for large v (s is 0 where e is infinite)

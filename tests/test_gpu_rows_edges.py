@@ -167,3 +167,29 @@ def test_gelu_tails(dt):
     rc.assert_close(out, v * cdf, rc.rounding(v * cdf, out.dtype) + rel * (v * cdf).abs(), "value")
     want = cdf + v * pdf
     rc.assert_close(slope, want, rc.rounding(want, out.dtype) + rel * (cdf + v.abs() * pdf), "slope")
+
+
+@pytest.mark.parametrize("act", rc.ACTS)
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_gated_nan_of_the_weights_shows(dt, act):
+    """A NaN in the gate's weights or bias alone reaches every row of its hidden
+    unit and, through it, every input gradient; other units stay clean.  Without an
+    activation the gate's own gradient, grad_out times up, does not hold the gate."""
+    n, c, h, dtype = 300, 72, 136, rc.DTYPES[dt]
+    x, dh = _randn(n, c, seed=1, dtype=dtype), _randn(n, h, seed=2, dtype=dtype)
+    W, b = _randn(2, c, h, seed=3, dtype=dtype), _randn(2, h, seed=4, dtype=dtype)
+    with _index(n) as idx:
+        clean, clean_grads = idx.gated_forward(x, W, b, act), idx.gated_backward(x, W, dh, b, act)
+        W[0, 5, 17] = float("nan")
+        b[0, 100] = float("nan")
+        out = idx.gated_forward(x, W, b, act)
+        dx, dW, db = idx.gated_backward(x, W, dh, b, act)
+    units = [17, 100]
+    rest = [u for u in range(h) if u not in units]
+    assert out[:, units].isnan().all() and torch.equal(out[:, rest], clean[:, rest])
+    assert dx.isnan().all()
+    first = 1 if act == "none" else 0
+    assert dW[first:, :, units].isnan().all() and db[first:, units].isnan().all()
+    assert torch.equal(dW[:, :, rest], clean_grads[1][:, :, rest])
+    assert torch.equal(db[:, rest], clean_grads[2][:, rest])
+    assert torch.equal(dW[:first], clean_grads[1][:first])
