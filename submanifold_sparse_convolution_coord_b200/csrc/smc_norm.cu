@@ -369,16 +369,17 @@ k_norm_bwd(const T* __restrict__ x, const float* __restrict__ gamma, const T* __
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const float2 d = g[p];
+        xc[p] = mul2(xc[p], rr);  // xhat: products with the inverse root's powers could overflow
         db[p] = add2(db[p], d);
-        dg[p] = fma2(mul2(d, rr), xc[p], dg[p]);
+        dg[p] = fma2(d, xc[p], dg[p]);
         const float2 q = mul2(d, gm[p]);
         s1 = add2(s1, q);
         s2 = fma2(q, xc[p], s2);
         if (kKeep) g[p] = q;
       }
       const float2 sums = group_sum2<G>(make_float2(s1.x + s1.y, s2.x + s2.y), nullptr);
-      // dx = r g - r mean(g) - xc r^3 mean(g xc)
-      const float k1 = -sums.x * inv_c * rstd, k2 = -sums.y * inv_c * rstd * rstd * rstd;
+      // dx = r g - r mean(g) - xhat r mean(g xhat)
+      const float k1 = -sums.x * inv_c * rstd, k2 = -sums.y * inv_c * rstd;
       const float2 kk1 = make_float2(k1, k1), kk2 = make_float2(k2, k2);
       if constexpr (!kKeep) {
         S::load(ds + row * c, lane, c, g);

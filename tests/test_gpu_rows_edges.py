@@ -193,3 +193,19 @@ def test_gated_nan_of_the_weights_shows(dt, act):
     assert torch.equal(dW[:, :, rest], clean_grads[1][:, :, rest])
     assert torch.equal(db[:, rest], clean_grads[2][:, rest])
     assert torch.equal(dW[:first], clean_grads[1][:first])
+
+
+@pytest.mark.parametrize("c", [64, 96, 515, 1024, 1200, 4099])
+@pytest.mark.parametrize("spread,size", [(1e-18, 1e4), (1e-16, 1e8), (1e17, 1e-6), (1e15, 1.0)])
+def test_norm_backward_of_extreme_spread(c, spread, size):
+    """Without eps the result scales with size / spread: what is computed on the
+    way stays in range.  Bound: as many roundings as the sums have, relative to
+    the row's largest term."""
+    x, dy = _randn(20, c, seed=1), _randn(20, c, seed=2) * size
+    x = x * spread
+    gamma = _randn(c, seed=3)
+    dx, dgamma, _ = smc_layer_norm_backward(x, gamma, dy, 0.0)
+    ref, rgamma, _ = rc.norm_grads(x, gamma, dy, 0.0)
+    bound = 400 * rc.E32 * ref.abs().amax(1, keepdim=True) + 1e-36
+    rc.assert_close(dx, ref, bound.expand_as(ref), "grad_in")
+    rc.assert_close(dgamma, rgamma, 400 * rc.E32 * rgamma.abs().max().expand_as(rgamma), "grad_gamma")
