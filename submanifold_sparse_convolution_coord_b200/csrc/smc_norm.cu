@@ -76,6 +76,15 @@ __device__ __forceinline__ float2 group_sum2(float2 v, float2* smem) {
   return v;
 }
 
+// sum / c by c's rounded reciprocal, corrected by what it leaves: a row whose
+// values are all alike, and whose sum is exact, has that value as its mean and so
+// xhat = 0.  (Without the correction x - sum * inv_c leaves up to 2^-24 of x, which
+// eps = 1e-5 lets through as an xhat of up to 0.02 for rows of 1000.)
+__device__ __forceinline__ float mean_of(float sum, int c, float inv_c) {
+  const float m = sum * inv_c;
+  return fmaf(fmaf(-m, float(c), sum), inv_c, m);
+}
+
 // A group's share of a row in registers.
 template <class T, int V, int G, int VECS>
 struct RowShare {
@@ -103,7 +112,7 @@ __device__ __forceinline__ float2 share_stats(const RowShare<T, V, G, VECS>& x, 
   for (int i = 0; i < VECS; ++i)
 #pragma unroll
     for (int j = 0; j < V; ++j) s += x.value(i, j);  // 0 outside the row
-  const float mean = group_sum<G>(s, smem) * inv_c;
+  const float mean = mean_of(group_sum<G>(s, smem), c, inv_c);
   s = 0.f;
 #pragma unroll
   for (int i = 0; i < VECS; ++i)
@@ -236,7 +245,7 @@ k_norm(const T* x, const float* __restrict__ gamma, const float* __restrict__ be
     const int r = group + k * kGroups;
     float2 v[P];
     S::expand(raw[k], v);
-    const float mean = group_sum<G>(S::sum(v), smem) * inv_c;
+    const float mean = mean_of(group_sum<G>(S::sum(v), smem), c, inv_c);
     const float squares = S::centre(v, mean, lane, c);
     const float rstd = rsqrtf(group_sum<G>(squares, smem) * inv_c + eps);
     if (r >= rows_here) continue;
@@ -359,7 +368,7 @@ k_norm_bwd(const T* __restrict__ x, const float* __restrict__ gamma, const T* __
       const bool ok = r < n;
       float2 xc[P], g[P];
       S::load(xs + row * c, lane, c, xc);
-      const float mean = group_sum<G>(S::sum(xc), nullptr) * inv_c;
+      const float mean = mean_of(group_sum<G>(S::sum(xc), nullptr), c, inv_c);
       const float squares = S::centre(xc, mean, lane, c);
       float rstd = rsqrtf(group_sum<G>(squares, nullptr) * inv_c + eps);
       if (!ok) rstd = 0.f;  // a row that does not exist: eps = 0 made it infinite

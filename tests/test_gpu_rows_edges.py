@@ -209,3 +209,22 @@ def test_norm_backward_of_extreme_spread(c, spread, size):
     bound = 400 * rc.E32 * ref.abs().amax(1, keepdim=True) + 1e-36
     rc.assert_close(dx, ref, bound.expand_as(ref), "grad_in")
     rc.assert_close(dgamma, rgamma, 400 * rc.E32 * rgamma.abs().max().expand_as(rgamma), "grad_gamma")
+
+
+@pytest.mark.parametrize("c", [49, 64, 98, 515, 784, 1024, 1200, 4099])
+def test_norm_of_constant_rows_is_beta(c):
+    """Rows whose values are all alike, and whose sum fp32 holds exactly: the mean
+    is that value exactly, so the result is beta and xhat is 0."""
+    for dt in ("f32", "f16", "bf16"):
+        dtype = rc.DTYPES[dt]
+        x = torch.tensor([2.5, 100, -7, 1000, -0.375, 3, 48, 2000], device=DEV).to(dtype)
+        x = x[:, None].expand(8, c).contiguous()
+        gamma, beta, dy = _randn(c, seed=1), _randn(c, seed=2), _randn(8, c, seed=3, dtype=dtype)
+        y = smc_layer_norm(x, gamma, beta, 1e-5)
+        assert torch.equal(y, beta.to(dtype).expand(8, c))
+        dx, dgamma, dbeta = smc_layer_norm_backward(x, gamma, dy, 1e-5)
+        assert not dgamma.any()
+        g = dy.double() * gamma.double()
+        want = (g - g.mean(1, keepdim=True)) * 1e-5 ** -0.5
+        size = (g.abs() + g.abs().mean(1, keepdim=True)) * 1e-5 ** -0.5
+        rc.assert_close(dx, want, rc.rounding(want, dtype) + 80 * rc.E32 * size)
