@@ -591,13 +591,15 @@ k_norm_bwd_long(const T* x, const float* gamma, const T* dy, T* dx, float2* stat
 
 constexpr int kColRows = 256;  // rows per partial sum of the column kernel
 
-// Partial sums of dgamma and dbeta: block (column strip, row chunk).
+// Partial sums of dgamma and dbeta: a block takes 256 columns of a row chunk.
+// The chunks are in the grid's first dimension, the only one that holds 2^31 rows'.
 template <class T>
 __global__ void __launch_bounds__(kThreads)
 k_norm_cols(const T* x, const T* dy, const float2* stats, float* part, int64_t n, int64_t c) {
-  const int64_t j = blockIdx.x * int64_t(kThreads) + threadIdx.x;
+  const unsigned strips = unsigned((c + kThreads - 1) / kThreads), chunk = blockIdx.x / strips;
+  const int64_t j = blockIdx.x % strips * int64_t(kThreads) + threadIdx.x;
   if (j >= c) return;
-  const int64_t r0 = blockIdx.y * int64_t(kColRows), r1 = min(n, r0 + kColRows);
+  const int64_t r0 = chunk * int64_t(kColRows), r1 = min(n, r0 + kColRows);
   float dg = 0.f, db = 0.f;
   for (int64_t r = r0; r < r1; ++r) {
     const float2 st = stats[r];
@@ -605,8 +607,8 @@ k_norm_cols(const T* x, const T* dy, const float2* stats, float* part, int64_t n
     dg += g * ((rows::to_float(x[r * c + j]) - st.x) * st.y);
     db += g;
   }
-  part[(blockIdx.y * int64_t(2) + 0) * c + j] = dg;
-  part[(blockIdx.y * int64_t(2) + 1) * c + j] = db;
+  part[(chunk * int64_t(2) + 0) * c + j] = dg;
+  part[(chunk * int64_t(2) + 1) * c + j] = db;
 }
 
 // dgamma and dbeta from the partial sums: a block takes 32 of the 2 c columns,
@@ -841,10 +843,13 @@ int layer_norm_backward(const void* x, const float* gamma, const void* dy, void*
       float2* stats = static_cast<float2*>(workspace);
       part = reinterpret_cast<float*>(stats + n);
       k_norm_bwd_long<T><<<unsigned(n), kThreads, 0, s>>>(in, gamma, g_out, g_in, stats, c, eps);
+      if (launched() != SMC_OK) return int(SMC_ERR_CUDA);
       if (dgamma) {
         parts = chunks(n);
-        k_norm_cols<T><<<dim3(unsigned((c + kThreads - 1) / kThreads), unsigned(parts)), kThreads,
-                         0, s>>>(in, g_out, stats, part, n, c);
+        // n c <= 2^44: at most 2^28 blocks and one more per strip and per chunk
+        const int64_t blocks = (c + kThreads - 1) / kThreads * parts;
+        k_norm_cols<T><<<unsigned(blocks), kThreads, 0, s>>>(in, g_out, stats, part, n, c);
+        if (launched() != SMC_OK) return int(SMC_ERR_CUDA);
       }
     } else if (n > 0) {
       if (dgamma) parts = p.blocks;

@@ -228,3 +228,21 @@ def test_norm_of_constant_rows_is_beta(c):
         want = (g - g.mean(1, keepdim=True)) * 1e-5 ** -0.5
         size = (g.abs() + g.abs().mean(1, keepdim=True)) * 1e-5 ** -0.5
         rc.assert_close(dx, want, rc.rounding(want, dtype) + 80 * rc.E32 * size)
+
+
+def test_norm_backward_of_very_many_long_rows():
+    """More rows than 65,535 times the 256 of a partial sum, of a length that the
+    kernels read again from cache (69 GB of rows and as much of gradients).
+    All ones: grad_beta is the number of rows, xhat is 0."""
+    n, c = 65_535 * 256 + 300, 2049
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 4 * n * c + 6 * 2 ** 30:
+        pytest.skip("needs 143 GB of free memory")
+    x = torch.ones(n, c, dtype=torch.bfloat16, device=DEV)
+    dx, dgamma, dbeta = smc_layer_norm_backward(x, torch.ones(c, device=DEV), x)
+    # sums of 256 ones are exact, and so are those of every 32nd of them; the 32
+    # sums of 2^19 or so add up to more than 2^24: half a step each
+    assert float((dbeta.double() - n).abs().max()) <= 32 and not dgamma.any()
+    assert not dx[:100].any() and not dx[n - 100:].any()
+    del x, dx
+    torch.cuda.empty_cache()
