@@ -702,45 +702,42 @@ Deal deal_bwd(I c, int elem) {
   return d;
 }
 
-// f(V, G, VECS) as compile-time values.
+// Whether deal (deal_bwd) gives K vectors of V values to each of G threads for
+// any row: kernels exist for these only.  Vectors narrower than 16 bytes come in
+// odd numbers, as a wider one would divide the row otherwise.
+template <class T, bool BWD>
+constexpr bool dealt(int v, int g, int k) {
+  if (v * int(sizeof(T)) < 16 && g == 2) return false;
+  if (v * int(sizeof(T)) < 8) {
+    if (g == 32) return k == 1 || k == 2 || (k % 4 == 0 && k <= 20);
+    return g < 32 ? k == 1 : g == kThreads && (k == 4 || k == 8);
+  }
+  if (g > 32) return k == 3 || k == 4;
+  if (BWD && g >= 16) return k == 2 || (g == 32 && (k == 3 || k == 4));
+  if (BWD && g == 8) return k <= 2;
+  return k == 1 || (g == 32 && k <= 4);
+}
+
+// f(V, G, K) as compile-time values.
 template <class T, bool BWD, class F>
 int by_deal(const Deal& d, F&& f) {
-#define SMC_VECS(K) \
-  case K:           \
-    return f(v, g, std::integral_constant<int, K>())
   auto with = [&](auto v, auto g) -> int {
     constexpr int V = decltype(v)::value, G = decltype(g)::value;
-    constexpr bool narrow = V * sizeof(T) < 8;
-    if constexpr (G < 32) {
-      if constexpr (BWD && !narrow && G >= 8)
-        if (d.vecs == 2) return f(v, g, std::integral_constant<int, 2>());
-      if (d.vecs == 1) return f(v, g, std::integral_constant<int, 1>());
-    } else if constexpr (!narrow) {
-      switch (d.vecs) {
-        SMC_VECS(1);
-        SMC_VECS(2);
-        SMC_VECS(3);
-        SMC_VECS(4);
-      }
-    } else if constexpr (G == 32) {
-      switch (d.vecs) {
-        SMC_VECS(1);
-        SMC_VECS(2);
-        SMC_VECS(4);
-        SMC_VECS(8);
-        SMC_VECS(12);
-        SMC_VECS(16);
-        SMC_VECS(20);
-      }
-    } else if constexpr (G == kThreads) {
-      switch (d.vecs) {
-        SMC_VECS(4);
-        SMC_VECS(8);
-      }
-    }
-    return int(SMC_ERR_INVALID);
+    int rc = SMC_ERR_INVALID;
+    auto one = [&](auto k) {
+      if constexpr (dealt<T, BWD>(V, G, decltype(k)::value))
+        if (d.vecs == decltype(k)::value) rc = f(v, g, k);
+    };
+    one(std::integral_constant<int, 1>());
+    one(std::integral_constant<int, 2>());
+    one(std::integral_constant<int, 3>());
+    one(std::integral_constant<int, 4>());
+    one(std::integral_constant<int, 8>());
+    one(std::integral_constant<int, 12>());
+    one(std::integral_constant<int, 16>());
+    one(std::integral_constant<int, 20>());
+    return rc;
   };
-#undef SMC_VECS
   auto wide = [&](auto v) -> int {
     switch (d.g) {
       case 1: return with(v, std::integral_constant<int, 1>());
@@ -761,6 +758,21 @@ int by_deal(const Deal& d, F&& f) {
     default:
       if constexpr (sizeof(T) == 2) return wide(std::integral_constant<int, 8>());
       return int(SMC_ERR_INVALID);
+  }
+}
+
+// run(WHOLE): rows that fill every thread's share (`whole`) are the common ones
+// and go without masks, from vectors of 8 bytes on.  Shares of one or two vectors
+// a row are always full; vectors narrower than 16 bytes, of which there is an odd
+// number, fill a share of one only.
+template <class T, int V, int G, class F>
+int by_fill(bool whole, F&& run) {
+  if constexpr (V * sizeof(T) >= 8 && G <= 2) {
+    return run(std::true_type());
+  } else {
+    if constexpr (V * sizeof(T) == 16)
+      if (whole) return run(std::true_type());
+    return run(std::false_type());
   }
 }
 
@@ -810,13 +822,12 @@ int layer_norm(const void* x, const float* gamma, const float* beta, void* out, 
     return by_deal<T, false>(d, [&](auto v, auto g, auto vecs) {
       constexpr int V = decltype(v)::value, G = decltype(g)::value, K = decltype(vecs)::value;
       const int64_t step = norm_threads<G>() / G * rows_per_group<T, V, K>();
-      // rows that fill every thread's share are the common ones: no masks
-      auto kern = k_norm<T, V, G, K, false>;
-      if constexpr (V * sizeof(T) >= 8)
-        if (c == G * K * V) kern = k_norm<T, V, G, K, true>;
-      kern<<<unsigned((n + step - 1) / step), norm_threads<G>(), 0, s>>>(
-          in, gamma, beta, o, n, int(c), 1.f / float(c), eps);
-      return launched();
+      return by_fill<T, V, G>(c == G * K * V, [&](auto whole) -> int {
+        k_norm<T, V, G, K, decltype(whole)::value>
+            <<<unsigned((n + step - 1) / step), norm_threads<G>(), 0, s>>>(
+                in, gamma, beta, o, n, int(c), 1.f / float(c), eps);
+        return launched();
+      });
     });
   });
 }
@@ -861,7 +872,7 @@ int layer_norm_backward(const void* x, const float* gamma, const void* dy, void*
               in, gamma, g_out, g_in, to, n, int(c), 1.f / float(c), eps);
           return launched();
         } else {
-          auto run = [&](auto whole) -> int {
+          return by_fill<T, V, G>(c == G * K * V, [&](auto whole) -> int {
             auto kern = k_norm_bwd<T, V, G, K, decltype(whole)::value>;
             constexpr int kMaxDev = 64;
             static bool attr_set[kMaxDev] = {};  // per device
@@ -877,11 +888,7 @@ int layer_norm_backward(const void* x, const float* gamma, const void* dy, void*
                 in, gamma, g_out, g_in, to, n, int(c), p.chunk_rows, p.slot_bytes, 1.f / float(c),
                 eps);
             return launched();
-          };
-          // rows that fill every thread's share are the common ones: no masks
-          if constexpr (V * sizeof(T) >= 8)
-            if (c == G * K * V) return run(std::true_type());
-          return run(std::false_type());
+          });
         }
       });
       if (rc != SMC_OK) return rc;

@@ -246,3 +246,25 @@ def test_norm_backward_of_very_many_long_rows():
     assert not dx[:100].any() and not dx[n - 100:].any()
     del x, dx
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_norm_of_every_length(dt):
+    """Each number of channels up to the longest rows of registers and some beyond
+    has a kernel; every 7th length is checked against float64."""
+    dtype = rc.DTYPES[dt]
+    n, most = 3, 4200
+    x = (_randn(n * most, seed=1) * 2 + 1).to(dtype)
+    dy = _randn(n * most, seed=2, dtype=dtype)
+    gamma, beta = _randn(most, seed=3), _randn(most, seed=4)
+    for c in range(1, most + 1):
+        a, d = x[:n * c].view(n, c), dy[:n * c].view(n, c)
+        g, b = gamma[:c], beta[:c]
+        y = smc_layer_norm(a, g, b, 1e-3)
+        grads = smc_layer_norm_backward(a, g, d, 1e-3)
+        if c % 7 != 1 and c > 40:
+            continue
+        rc.assert_close(y, rc.norm(a, g, b, 1e-3), rc.norm_bound(a, g, b, 1e-3, dtype), f"{c}")
+        for u, r, e in zip(grads, rc.norm_grads(a, g, d, 1e-3),
+                           rc.norm_grads_bound(a, g, d, 1e-3, dtype)):
+            rc.assert_close(u, r, e, f"{c} gradients")
