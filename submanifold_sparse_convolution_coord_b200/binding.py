@@ -428,9 +428,14 @@ def smc_layer_norm_backward_workspace(n: int, c: int, dtype: torch.dtype) -> int
 def smc_layer_norm_backward(x: torch.Tensor, gamma: Optional[torch.Tensor],
                             grad_out: torch.Tensor, eps: float = 1e-5,
                             grad_in: Optional[torch.Tensor] = None,
-                            stream: Optional[torch.cuda.Stream] = None) -> tuple:
+                            stream: Optional[torch.cuda.Stream] = None,
+                            param_grads: Optional[bool] = None) -> tuple:
     """Gradients of smc_layer_norm: (grad_in [N, C], grad_gamma, grad_beta
-    float32 [C]); the last two are None when gamma is None."""
+    float32 [C]); the last two are None without param_grads, which is by default
+    whether gamma is given.  A norm with beta alone asks for them with True
+    (grad_gamma is then that of a gamma of ones)."""
+    if param_grads is None:
+        param_grads = gamma is not None
     code = _rows(x, "x")
     n, c = x.shape
     xp = _dev_ptr(x, "x")
@@ -442,8 +447,9 @@ def smc_layer_norm_backward(x: torch.Tensor, gamma: Optional[torch.Tensor],
             grad_in = torch.empty_like(x)
             ip = grad_in.data_ptr()
         dgamma = dbeta = None
-        if gamma is not None:
-            dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
+        if param_grads:
+            dgamma = torch.empty(c, dtype=torch.float32, device=x.device)
+            dbeta = torch.empty_like(dgamma)
         size = smc_layer_norm_backward_workspace(n, c, x.dtype)
         work = torch.empty(size, dtype=torch.uint8, device=x.device)
         _check(lib().smc_layer_norm_backward(

@@ -268,3 +268,16 @@ def test_norm_of_every_length(dt):
         for u, r, e in zip(grads, rc.norm_grads(a, g, d, 1e-3),
                            rc.norm_grads_bound(a, g, d, 1e-3, dtype)):
             rc.assert_close(u, r, e, f"{c} gradients")
+
+
+def test_norm_backward_beta_without_gamma():
+    """A norm with beta alone has a gradient for it."""
+    x, dy = _randn(50, 96, seed=1), _randn(50, 96, seed=2)
+    plain = smc_layer_norm_backward(x, None, dy)
+    assert plain[1] is None and plain[2] is None
+    dx, dgamma, dbeta = smc_layer_norm_backward(x, None, dy, param_grads=True)
+    want = smc_layer_norm_backward(x, torch.ones(96, device=DEV), dy)
+    assert torch.equal(dx, plain[0]) and torch.equal(dx, want[0])
+    assert torch.equal(dgamma, want[1]) and torch.equal(dbeta, want[2])
+    dx, dgamma, dbeta = smc_layer_norm_backward(x, torch.ones(96, device=DEV), dy, param_grads=False)
+    assert torch.equal(dx, want[0]) and dgamma is None and dbeta is None
