@@ -29,7 +29,6 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "smc_internal.h"
 #include "smc_ptx.cuh"
@@ -1034,8 +1033,8 @@ k_join_dw(const float* __restrict__ slots, T* __restrict__ dW, int C, int H, int
   const I i0 = I(tile) * k_iters, i1 = i0 + k_iters;
   const int p0 = int(((i0 + 1) * pairs - 1) / all), p1 = int((i1 * pairs - 1) / all);
   if (p0 == p1) return;  // one pair stored it whole
-  // the first pair used its second slot if the tile starts its last segment
-  const int64_t first = 2 * int64_t(p0) + (p0 * all / pairs > i0 ? 0 : 1);
+  // the first pair has the tile's first stage, so its part is in its second slot
+  const int64_t first = 2 * int64_t(p0) + 1;
   tile %= 2 * m_tiles;
   const int64_t s = tile / m_tiles, h = int64_t(tile % m_tiles) * 256 + threadIdx.x;
   if (h >= H) return;
