@@ -281,3 +281,60 @@ def test_norm_backward_beta_without_gamma():
     assert torch.equal(dgamma, want[1]) and torch.equal(dbeta, want[2])
     dx, dgamma, dbeta = smc_layer_norm_backward(x, torch.ones(96, device=DEV), dy, param_grads=False)
     assert torch.equal(dx, want[0]) and dgamma is None and dbeta is None
+
+
+def _exact(a, b):
+    """a^T b of small whole numbers, exact in float64, in pieces of the rows."""
+    return sum(a[r:r + 200_000].double().t() @ b[r:r + 200_000].double()
+               for r in range(0, a.shape[0], 200_000))
+
+
+@pytest.mark.parametrize("n,c,h", [(30_001, 128, 200), (1_100_000, 16, 2048), (150_001, 264, 600)])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_gated_sums_over_rows_are_exact(dt, n, c, h):
+    """Whole numbers whose sums fp32 holds exactly, whatever the order: grad_W and
+    grad_bias equal the sums rounded once.  A share of the rows that is lost,
+    taken twice or put into the wrong tile changes most entries."""
+    dtype = rc.DTYPES[dt]
+    x, dh = _signs(n, c, seed=5, dtype=dtype), _signs(n, h, seed=6, dtype=dtype)
+    W, b = _unit_gate(c, h, dtype)
+    with _index(n) as idx:
+        _, dW, db = idx.gated_backward(x, W, dh, b, "none")
+        assert idx.status() == 0
+    want, sums = _exact(x, dh).to(dtype), dh.double().sum(0).to(dtype)
+    for half in range(2):
+        assert torch.equal(dW[half], want) and torch.equal(db[half], sums)
+    # the rows of a sixty-fourth of the sum would show nearly everywhere
+    part = _exact(x[:n // 64], dh[:n // 64])
+    assert float(((want.double() - part).to(dtype) != want).float().mean()) > 0.9
+
+
+@pytest.mark.parametrize("n,c,dt", [(700_001, 16, "bf16"), (700_001, 16, "f32"), (50_001, 515, "f32"),
+                                    (60_001, 1200, "f16"), (20_001, 4099, "bf16"),
+                                    (33_600_000, 64, "bf16")])
+def test_norm_sums_over_rows_are_exact(n, c, dt):
+    """grad_beta of whole numbers is exact.  Rows of ones and minus ones around 0
+    have xhat = +-r for the same r, so grad_gamma is r times a whole number."""
+    dtype = rc.DTYPES[dt]
+    dy = _signs(n, c, seed=7, dtype=dtype)
+    x = torch.ones(c, dtype=dtype, device=DEV)
+    x[1::2] = -1
+    x[(c // 2) * 2:] = 0  # an odd channel
+    x = x.expand(n, c).contiguous()
+    x[n // 3:n // 2] *= -1
+    var = (c // 2) * 2 / c
+    _, dgamma, dbeta = smc_layer_norm_backward(x, torch.ones(c, device=DEV), dy, 0.5)
+    want = torch.zeros(c, dtype=torch.float64, device=DEV)
+    products = want.clone()
+    for r in range(0, n, 1_000_000):
+        d = dy[r:r + 1_000_000].double()
+        want += d.sum(0)
+        products += (d * x[r:r + 1_000_000].double()).sum(0)
+    assert torch.equal(dbeta.double(), want)
+    products *= (var + 0.5) ** -0.5
+    # r: the variance, the sum with eps and the inverse root, each the same in every
+    # row; then a random walk of n steps of r stays below 3 sqrt(n) r, and its n
+    # roundings, of random sign, add up to at most 3 sqrt(n) times 2^-24 of that
+    bound = 8 * rc.E32 * products.abs() + 9 * n * rc.E32 * (var + 0.5) ** -0.5
+    rc.assert_close(dgamma, products, bound, "dgamma")
+    assert float((products.abs() > 4 * bound).float().mean()) > 0.9
