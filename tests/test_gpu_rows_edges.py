@@ -338,3 +338,61 @@ def test_norm_sums_over_rows_are_exact(n, c, dt):
     bound = 8 * rc.E32 * products.abs() + 9 * n * rc.E32 * (var + 0.5) ** -0.5
     rc.assert_close(dgamma, products, bound, "dgamma")
     assert float((products.abs() > 4 * bound).float().mean()) > 0.9
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_gated_bad_inputs_reach_the_weight_gradient(dt):
+    """A NaN in channel k of the input spoils its row's dg and du, so all of
+    grad_W and grad_bias; one in grad_out spoils its unit's column only."""
+    n, c, h, dtype = 300, 72, 136, rc.DTYPES[dt]
+    x, dh = _randn(n, c, seed=1, dtype=dtype), _randn(n, h, seed=2, dtype=dtype)
+    W, b = _randn(2, c, h, seed=3, dtype=dtype), _randn(2, h, seed=4, dtype=dtype)
+    with _index(n) as idx:
+        clean = idx.gated_backward(x, W, dh, b)
+        bad = x.clone()
+        bad[5, 3] = float("nan")
+        _, dW, db = idx.gated_backward(bad, W, dh, b)
+        assert dW.isnan().all() and db.isnan().all()
+        bad = dh.clone()
+        bad[299, 7] = float("nan")
+        dx, dW, db = idx.gated_backward(x, W, bad, b)
+    rest = [u for u in range(h) if u != 7]
+    assert dx[299].isnan().all() and torch.equal(dx[:299], clean[0][:299])
+    assert dW[:, :, 7].isnan().all() and torch.equal(dW[:, :, rest], clean[1][:, :, rest])
+    assert db[:, 7].isnan().all() and torch.equal(db[:, rest], clean[2][:, rest])
+
+
+def test_captured_after_other_work():
+    """A chain whose kernels are placed early may follow anything in a captured
+    graph: a memory copy, a memset, a join of two streams, nothing at all."""
+    n, c, h = 500, 100, 64
+    x, W = _randn(n, c, seed=1, dtype=torch.float16), _randn(2, c, h, seed=2, dtype=torch.float16)
+    dh, gamma = _randn(n, h, seed=3, dtype=torch.float16), torch.ones(c, device=DEV)
+    with _index(n) as idx, SubMIndex(torch.zeros(0, 4, dtype=torch.int32, device=DEV)) as none:
+        want = idx.gated_forward(x, W)
+        grads = idx.gated_backward(x, W, dh)[:2]
+        torch.cuda.synchronize()
+        buf, zeros = torch.zeros_like(x), torch.ones_like(x)
+        side = torch.cuda.Stream()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            first = smc_layer_norm_backward(x[:0], gamma, x[:0])  # the join alone
+            buf.copy_(x)
+            a = idx.gated_forward(buf, W)
+            zeros.zero_()
+            b = idx.gated_backward(buf, W, dh)[:2]
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                d = smc_layer_norm(x, gamma)
+            e = smc_layer_norm(x, gamma)
+            torch.cuda.current_stream().wait_stream(side)
+            f = idx.gated_forward(buf, W)
+        for _ in range(3):
+            for t in (buf, a, *b, d, e, f, first[1]):
+                t.fill_(3)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(a, want) and torch.equal(f, want) and torch.equal(d, e)
+            assert all(torch.equal(u, v) for u, v in zip(b, grads)) and not first[1].any()
+        assert idx.status() == 0 and none.status() == 0
+        del g
