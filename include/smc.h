@@ -461,9 +461,13 @@ int smc_gated_forward(smc_handle_t h, const void* feats, const void* W, const vo
  * grad_bias : device pointer, [2][hidden] of dtype, or NULL.
  * Every element of the outputs that are given is overwritten (zeros in grad_W
  * and grad_bias for n = 0).  dg and du are rounded to dtype between the
- * products (SMC_F32: kept to fp32), all sums are fp32, each result is rounded
- * once to dtype.  grad_W is in dtype, not fp32 as smc_backward_weight's: it
- * carries the rounding of dg and du already.  relu'(0) = 0.  The sums over
+ * products (SMC_F32: kept to fp32), which adds an error of the size of the
+ * results' own rounding to grad_in and grad_W (grad_bias is summed before it).
+ * In SMC_F16 a dg or du beyond 65,504 is infinite in the products of its row and
+ * its hidden unit, and one below 2^-24 is lost: scale grad_out, as for any fp16
+ * gradient.  All sums are fp32, each result is rounded once to dtype.  grad_W is
+ * in dtype, not fp32 as smc_backward_weight's: it carries the rounding of dg and
+ * du already.  relu'(0) = 0.  The sums over
  * rows are split over CTAs and joined in a fixed order, without atomics: the
  * same call gives the same bits.  Asynchronous on stream.
  * Errors: as smc_gated_forward, outputs that overlap each other included.

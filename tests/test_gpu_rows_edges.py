@@ -396,3 +396,26 @@ def test_captured_after_other_work():
             assert all(torch.equal(u, v) for u, v in zip(b, grads)) and not first[1].any()
         assert idx.status() == 0 and none.status() == 0
         del g
+
+
+def test_gated_fp16_gradient_out_of_range():
+    """dg and du are fp16 between the products: a dg beyond 65,504 is infinite
+    and shows in its row's and its unit's gradients, and in no others; the same
+    gradient scaled down by 2^-8 is right (what loss scaling does)."""
+    n, c, h = 200, 64, 96
+    x, W = _randn(n, c, seed=1, dtype=torch.float16), _randn(2, c, h, seed=2) / 8
+    W, b = W.half(), _randn(2, h, seed=3, dtype=torch.float16)
+    dh = _randn(n, h, seed=4, dtype=torch.float16)
+    b[:, 11] = 100.0  # u = 100 or so, its gate's slope 1
+    dh[20, 11] = 3000.0
+    with _index(n) as idx:
+        dx, dW, db = idx.gated_backward(x, W, dh, b)
+        small = (dh.float() / 256).half()
+        got = idx.gated_backward(x, W, small, b)
+    rows, units = [r for r in range(n) if r != 20], [u for u in range(h) if u != 11]
+    assert not torch.isfinite(dx[20]).any() and torch.isfinite(dx[rows]).all()
+    assert not torch.isfinite(dW[:, :, 11]).any() and torch.isfinite(dW[:, :, units]).all()
+    assert torch.isinf(db[:, 11]).all() and torch.isfinite(db[:, units]).all()
+    ref = rc.Gated(x, W, b, "silu", small)
+    for a, r, bound in zip(got, (ref.dx, ref.dW, ref.db), (ref.dx_bound, ref.dW_bound, ref.db_bound)):
+        rc.assert_close(a, r, bound)
