@@ -419,3 +419,47 @@ def test_gated_fp16_gradient_out_of_range():
     ref = rc.Gated(x, W, b, "silu", small)
     for a, r, bound in zip(got, (ref.dx, ref.dW, ref.db), (ref.dx_bound, ref.dW_bound, ref.db_bound)):
         rc.assert_close(a, r, bound)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n,c,h", [(5, 65536, 3), (5, 3, 65536), (300, 4160, 8), (70, 4104, 2056)])
+def test_gated_longest_sides(dt, n, c, h):
+    """The widest rows and hidden layers there may be, and sums just over a piece,
+    against float64 under the bounds of the ordinary shapes."""
+    dtype = rc.DTYPES[dt]
+    x, dh = _randn(n, c, seed=1, dtype=dtype), _randn(n, h, seed=2, dtype=dtype)
+    W = (_randn(2, c, h, seed=3) * c ** -0.5).to(dtype)
+    b = _randn(2, h, seed=4, dtype=dtype)
+    with _index(n) as idx:
+        ref = rc.Gated(x, W, b, "gelu", dh)
+        rc.assert_close(idx.gated_forward(x, W, b, "gelu"), ref.out, ref.out_bound, "out")
+        dx, dW, db = idx.gated_backward(x, W, dh, b, "gelu")
+        rc.assert_close(dx, ref.dx, ref.dx_bound, "grad_in")
+        rc.assert_close(dW, ref.dW, ref.dW_bound, "grad_W")
+        rc.assert_close(db, ref.db, ref.db_bound, "grad_bias")
+        assert idx.status() == 0
+
+
+def test_one_handle_on_two_streams():
+    """Calls on one handle from two streams at once, each with its own workspace."""
+    n, c, h = 6000, 136, 392
+    with _index(n) as idx:
+        sets = [(_randn(n, c, seed=k, dtype=torch.bfloat16), _randn(n, h, seed=9 + k, dtype=torch.bfloat16))
+                for k in range(2)]
+        W, b = _randn(2, c, h, seed=20, dtype=torch.bfloat16), _randn(2, h, seed=21, dtype=torch.bfloat16)
+
+        def step(x, dh):
+            return (idx.gated_forward(x, W, b),) + idx.gated_backward(x, W, dh, b)
+        want = [step(*s) for s in sets]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        got = [[], []]
+        for _ in range(8):
+            for k, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    got[k].append(step(*sets[k]))
+        torch.cuda.synchronize()
+        for k in range(2):
+            for outs in got[k]:
+                assert all(torch.equal(a, w) for a, w in zip(outs, want[k]))
+        assert idx.status() == 0
