@@ -364,7 +364,9 @@ int smc_forward_ex(smc_handle_t h, const void* feats, const void* W, void* out, 
  * Statistics and arithmetic are fp32; the result is rounded once to dtype.
  * A row's result depends on that row alone (an infinite or NaN value makes
  * its own row NaN and no other; a row whose squared deviations pass the range
- * of fp32 gives beta).  Asynchronous on stream; no workspace.
+ * of fp32 gives beta, one whose sum does NaN; one whose values are all alike,
+ * with a sum that fp32 holds, gives beta for eps > 0).  Asynchronous on stream; no
+ * workspace.
  * Errors: SMC_ERR_INVALID (null or misaligned pointers, bad sizes, dtype or
  * eps, out overlapping an input in any other way), SMC_ERR_UNSUPPORTED (n or
  * c >= 2^31), SMC_ERR_CUDA.
@@ -407,9 +409,9 @@ int smc_layer_norm_backward_workspace(int64_t n, int64_t c, int dtype, int64_t* 
 
 /*
  * Gated feed-forward product over the handle's rows: the first half of a
- * gated SparseFeedForwardNet (trellis_sparse_mlx README, "What's in it"), two
- * per-row linear maps of the same input, the activation and the product in
- * one pass:
+ * feed-forward block (trellis_sparse_mlx README, "What's in it", names a
+ * SparseFeedForwardNet; the gate is this library's choice), two per-row linear
+ * maps of the same input, the activation and the product in one pass:
  *
  *     out = act(feats @ W[0] + bias[0]) * (feats @ W[1] + bias[1])
  *

@@ -463,7 +463,7 @@ __device__ __forceinline__ void biased8(const uint32_t* gv, const uint32_t* uv, 
 // them with 16-bit W and x.  That adds as much error to dx and dW as their own
 // rounding does (55,100 rows 512 -> 2048 bf16: 2.3e-3 in place of 1.7e-3 of the
 // values' size); a second 16-bit part of dg and du would take it away at twice
-// the products of dx and dW, which are 315 of the call's 570 us of kernels.
+// the products of dx and dW, which are 333 of the call's 570 us of kernels.
 template <int MODE, int DT, int ACT, bool BIAS>
 __device__ __forceinline__ void gate8(const uint32_t* gv, const uint32_t* uv, int g8,
                                       const GateRow& c) {
