@@ -560,10 +560,12 @@ template <int MODE, int DT>
 __device__ __forceinline__ void gate16(const uint32_t (&gv)[16], const uint32_t (&uv)[16], int hf,
                                        int act, const GateRow& c) {
   auto go = [&](auto a, auto b) {
-    if constexpr (MODE == kPreBwd && DT == SMC_F32)
-      return gate16_parts<decltype(a)::value, decltype(b)::value>(gv, uv, hf, c);
-    gate8<MODE, DT, decltype(a)::value, decltype(b)::value>(gv, uv, 2 * hf, c);
-    gate8<MODE, DT, decltype(a)::value, decltype(b)::value>(gv + 8, uv + 8, 2 * hf + 1, c);
+    if constexpr (MODE == kPreBwd && DT == SMC_F32) {
+      gate16_parts<decltype(a)::value, decltype(b)::value>(gv, uv, hf, c);
+    } else {
+      gate8<MODE, DT, decltype(a)::value, decltype(b)::value>(gv, uv, 2 * hf, c);
+      gate8<MODE, DT, decltype(a)::value, decltype(b)::value>(gv + 8, uv + 8, 2 * hf + 1, c);
+    }
   };
   auto choose = [&](auto b) {
     switch (act) {
